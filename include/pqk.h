@@ -448,6 +448,135 @@ PQK_API int pqk_linear_swiglu(const void* a, int64_t a_stride_t, const void* w1,
                               int64_t T, int K, int F, void* stream);
 
 /*
+ * pqk_norm_modulate_i8 -- the gated residual, norm and adaLN modulation of
+ * pqk_modulate_swiglu with an 8-bit output for the int8 linear layers below,
+ * so that h is neither written nor read as bf16 (residual connections,
+ * modulation and normalisation are among the operators the pages fuse: first
+ * page, section "融合 DiT 算子"; the 8-bit output is a reading, see
+ * pqk_linear_i8_gated_residual). For every token t of request s:
+ *   x'   = x[t] + gate_res[s] * branch[t]   (branch NULL: x' = x[t]; gate_res
+ *          NULL with a branch: x' = x[t] + branch[t])
+ *   h    = norm(x') * weight * (1 + scale[s]) + shift[s]  (pqk_norm_type over
+ *          C; weight NULL: 1; scale and shift NULL: norm(x') * weight)
+ *   h_scale[t] = max_c |h_c| / 127, or 1 when every h_c is 0
+ *   h8[t, c]   = h_c / h_scale[t] rounded to the nearest integer, ties to
+ *                even, so in -127..127
+ * fp32 arithmetic; h is not rounded before it is coded. A token with an
+ * infinite or NaN h_c (or whose mean square passes fp32's range) gets h_scale
+ * NaN and codes 0: its dequantised row is NaN, the other tokens' are not
+ * affected.
+ *
+ * x, branch     device bf16 [T, C], rows x_stride_t / branch_stride_t apart.
+ * x_out         device bf16 [T, C] receiving x', rows x_out_stride_t apart, or
+ *               NULL; may equal x or branch (same stride).
+ * h8            device int8 [T, C], rows h8_stride_t bytes apart, a multiple
+ *               of 8 (of 16 to be read by the linear layers); what lies
+ *               between the rows is left as it is.
+ * h_scale       device fp32 [T], 4-byte aligned.
+ * weight        device bf16 [C] or NULL.
+ * shift, scale  device fp32 [B, C], both or neither; gate_res device fp32
+ *               [B, C] or NULL (NULL without a branch).
+ * cu_seqlens    device int32 [B+1] (must be valid; not re-checked here); with
+ *               shift and gate_res both NULL it is not read and may be NULL.
+ * C             a multiple of 8, at most 16384. 0 <= T <= 2^31 - 513. eps > 0.
+ */
+PQK_API int pqk_norm_modulate_i8(const void* x, int64_t x_stride_t, const void* branch, int64_t branch_stride_t,
+                                 void* x_out, int64_t x_out_stride_t, void* h8, int64_t h8_stride_t, float* h_scale,
+                                 const void* weight, const float* shift, const float* scale, const float* gate_res,
+                                 const int32_t* cu_seqlens, int B, int64_t T, int C, int norm_type, float eps,
+                                 void* stream);
+
+/*
+ * pqk_quantize_i8 -- the rows of a bf16 tensor as int8 codes with one scale
+ * per row, the rule of pqk_norm_modulate_i8 with h = x: an attention's output
+ * or a SwiGLU's in front of an int8 linear layer, and (rows being output
+ * channels) the layer's weight.
+ *
+ * x       device bf16 [T, C], rows x_stride_t apart.
+ * x8      device int8 [T, C], rows x8_stride_t apart; scales device fp32 [T].
+ * Sizes and alignment as pqk_norm_modulate_i8.
+ */
+PQK_API int pqk_quantize_i8(const void* x, int64_t x_stride_t, int64_t T, int C, void* x8, int64_t x8_stride_t,
+                            float* scales, void* stream);
+
+/*
+ * pqk_linear_i8_gated_residual -- pqk_linear_gated_residual with both operands
+ * in 8-bit integers, one scale per token and one per output channel (the
+ * second page's bullet "Sparse & quantized attention" quantises the attention
+ * only; 8-bit linear layers around it are a reading). For every token t of
+ * request s:
+ *   y[t, n]   = a_scale[t] * w_scale[n] * sum_k a8[t, k] * w8[n, k]
+ *   out[t, n] = x[t, n] + gate_res[s, n] * y[t, n]
+ * With x and gate_res both NULL: out = y. The sums are exact (int32); they are
+ * scaled in fp32 and out is rounded to bf16 (nearest even).
+ *
+ * a8          device int8 [T, K], rows a8_stride_t bytes apart (a multiple of
+ *             16, as pqk_norm_modulate_i8 and pqk_quantize_i8 write them).
+ * a_scale     device fp32 [T], 4-byte aligned.
+ * w8          device int8 [N, K] (out x in features), rows w8_stride_n bytes
+ *             apart (a multiple of 16).
+ * w_scale     device fp32 [N], 16-byte aligned.
+ * x, gate_res, cu_seqlens, out: as pqk_linear_gated_residual.
+ * K, N        multiples of 8, >= 8; K <= 131071 (the sums fit in int32 for
+ *             codes of -128 too); T, N limits as pqk_linear_gated_residual.
+ * Errors as pqk_linear_gated_residual.
+ */
+PQK_API int pqk_linear_i8_gated_residual(const void* a8, int64_t a8_stride_t, const float* a_scale, const void* w8,
+                                         int64_t w8_stride_n, const float* w_scale, const void* x,
+                                         int64_t x_stride_t, const float* gate_res, const int32_t* cu_seqlens, int B,
+                                         void* out, int64_t out_stride_t, int64_t T, int K, int N, void* stream);
+
+/*
+ * pqk_linear_i8_swiglu -- pqk_linear_swiglu with 8-bit operands: with y as in
+ * pqk_linear_i8_gated_residual on w8's 2F rows (the SiLU operand's F rows
+ * first), act[t, f] = silu(y[t, f]) * y[t, F + f].
+ *
+ * a8, a_scale  as pqk_linear_i8_gated_residual.
+ * w8           device int8 [2F, K], rows w8_stride_n apart; w_scale [2F].
+ * act          device bf16 [T, F], rows act_stride_t apart.
+ */
+PQK_API int pqk_linear_i8_swiglu(const void* a8, int64_t a8_stride_t, const float* a_scale, const void* w8,
+                                 int64_t w8_stride_n, const float* w_scale, void* act, int64_t act_stride_t,
+                                 int64_t T, int K, int F, void* stream);
+
+/*
+ * pqk_varlen_cross_attn_fwd -- packed attention to another packed sequence:
+ * the tokens of a request attend to all of that request's keys, which come
+ * from an encoder (a text prompt's states) or another modality (audio to
+ * video), with lengths of their own, and to nothing else. As with
+ * pqk_varlen_attn_fwd nothing is padded ("Long-sequence attention &
+ * communication": only valid tokens are processed); that the conditioning
+ * enters by cross-attention is a reading.
+ *   O = softmax(softmax_scale * Q K^T) V over the request's keys, bf16
+ *   operands, fp32 accumulation, probabilities rounded to bf16 for P V.
+ * A request without keys gives O = 0 and lse = -inf for its queries.
+ *
+ * q, o          device bf16 [Tq, H, D]; k, v device bf16 [Tk, Hkv, D], Hkv a
+ *               divisor of H (query head h reads key head h / (H / Hkv)), rows
+ *               *_stride_t elements apart (k and v may be NULL when Tk is 0).
+ *               o may not overlap an input.
+ * lse           device fp32 [H, Tq] natural log-sum-exp, or NULL; 4-byte
+ *               aligned.
+ * cu_seqlens_q, cu_seqlens_k  device int32 [B+1], from 0, monotone, ending at
+ *               or before Tq / Tk (else nothing is written and the status word
+ *               becomes PQK_ERR_BAD_SEQLENS). Rows of o (columns of lse)
+ *               behind the last request are left as they are; rows of k and v
+ *               behind it, and other requests' rows, never reach a result,
+ *               whatever they hold.
+ * workspace     device, 16-byte aligned, at least
+ *               pqk_varlen_cross_attn_workspace_size(B, D) bytes (0 for an
+ *               unsupported B or D); contents need not be kept between calls,
+ *               calls that may overlap on the GPU need one each.
+ * D 64 or 128; (ceil(Tq/256) + B) * H below 2^31 - 2^20; Tq, Tk <= 2^31 - 513.
+ */
+PQK_API size_t pqk_varlen_cross_attn_workspace_size(int B, int D);
+PQK_API int pqk_varlen_cross_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                                      int64_t q_stride_t, int64_t k_stride_t, int64_t v_stride_t,
+                                      int64_t o_stride_t, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                      int B, int64_t Tq, int64_t Tk, int H, int Hkv, int D, float softmax_scale,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * pqk_get_device_status -- synchronises `stream`, then returns and clears
  * the current device's status word: PQK_OK, PQK_ERR_TIMEOUT or
  * PQK_ERR_BAD_SEQLENS (the first condition recorded since the last read),

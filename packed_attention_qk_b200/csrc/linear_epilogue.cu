@@ -10,6 +10,12 @@
 //   kEpiSwiglu         out[t, f] = silu((A W_gate^T)[t, f]) * (A W_up^T)[t, f]
 //   kEpiNone           out = A W^T
 //
+// kI8: A and W are signed 8-bit codes with one scale per token and one per W
+// row (kind::i8, int32 accumulation, which is exact); the accumulator times
+// the two scales takes the place of (A W^T) above. A 128-byte swizzle row then
+// holds 128 K positions instead of 64, and everything between the tensor maps
+// and the accumulator is the same.
+//
 // A: [T, K] bf16 (token stride a_stride), W: [N, K] bf16 (out x in). fp32
 // accumulation in tensor memory, epilogue arithmetic in fp32, bf16 output
 // rounded to nearest even.
@@ -59,14 +65,14 @@ namespace pqk {
 namespace {
 
 constexpr int kBM = 128;       // token rows per CTA (pair: 256)
-constexpr int kBK = 64;        // K per stage: one 128-byte swizzle row of bf16
+constexpr int kRowBytes = 128; // K per stage: one 128-byte swizzle row, 64 bf16 or 128 int8
 constexpr int kBoxRows = 128;  // W rows per CTA and stage
 constexpr int kAccCols = 256;  // fp32 accumulator columns per tile = MMA N
 constexpr int kStages = 6;
 constexpr int kThreads = 192;
 constexpr int kGroupM = 8;     // raster: pair M tiles per group
-constexpr uint32_t kABytes = kBM * kBK * 2;        // 16 KB
-constexpr uint32_t kBBytes = kBoxRows * kBK * 2;   // 16 KB
+constexpr uint32_t kABytes = kBM * kRowBytes;        // 16 KB
+constexpr uint32_t kBBytes = kBoxRows * kRowBytes;   // 16 KB
 constexpr uint32_t kPairStageBytes = 2 * (kABytes + kBBytes);
 
 struct Layout {
@@ -89,10 +95,12 @@ struct Params {
   int64_t x_stride;
   const float* gate_res;    // [B, N]
   const int32_t* cu;        // [B + 1]
+  const float* a_scale;     // kI8: [T]
+  const float* w_scale;     // kI8: [N] ([2N] for SwiGLU, gate rows first)
   int B;
   int64_t T;
   int N;                    // output columns (F for SwiGLU)
-  int n_kb;                 // K blocks of 64
+  int n_kb;                 // K blocks of one swizzle row
   int m_pairs;              // 256-token tiles
   int n_tiles;
   int* status;
@@ -132,11 +140,31 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-template <int kEpi>
+// kCount consecutive accumulator columns as floats: as they are, or int32 sums
+// times the token's and the columns' scales (ws: the first column's).
+template <bool kI8, int kCount>
+__device__ __forceinline__ void acc_values(const uint32_t* acc, float row_scale, const float* ws, float (&o)[kCount]) {
+  if constexpr (kI8) {
+#pragma unroll
+    for (int e = 0; e < kCount; e += 4) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(ws + e));
+      o[e] = __int2float_rn(static_cast<int>(acc[e])) * row_scale * w.x;
+      o[e + 1] = __int2float_rn(static_cast<int>(acc[e + 1])) * row_scale * w.y;
+      o[e + 2] = __int2float_rn(static_cast<int>(acc[e + 2])) * row_scale * w.z;
+      o[e + 3] = __int2float_rn(static_cast<int>(acc[e + 3])) * row_scale * w.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kCount; ++e) o[e] = __uint_as_float(acc[e]);
+  }
+}
+
+template <int kEpi, bool kI8>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b0,
                        const __grid_constant__ CUtensorMap tm_b1, const Params p) {
   using L = Layout;
+  constexpr int kBlockK = kI8 ? kRowBytes : kRowBytes / 2;  // K positions per stage
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -219,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = mbar_wait(empty(s), round & 1, abort_flag, p.timeout_ns))) break;
           }
           const uint32_t bar = in_cta(full(s), 0);
-          tma_load_2d_pair(a_smem + s * kABytes, &tm_a, bar, kb * kBK, arow);
-          tma_load_2d_pair(b_smem + s * kBBytes, mb, bar, kb * kBK, brow);
+          tma_load_2d_pair(a_smem + s * kABytes, &tm_a, bar, kb * kBlockK, arow);
+          tma_load_2d_pair(b_smem + s * kBBytes, mb, bar, kb * kBlockK, brow);
           ++it;
         }
       }
@@ -229,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (even CTA)
     if (lane == 0 && even) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(2 * kBM, kAccCols, false);
+      constexpr uint32_t kIdesc = kI8 ? idesc_s8_s32(2 * kBM, kAccCols) : idesc_bf16_f32(2 * kBM, kAccCols, false);
       constexpr uint32_t kDescHi = smem_desc_hi_sw128(1024);
       const uint32_t a_lo = smem_desc_lo(a_smem, 16);
       const uint32_t b_lo = smem_desc_lo(b_smem, 16);
@@ -247,9 +275,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = mbar_wait(full(s), (it / kStages) & 1, abort_flag, p.timeout_ns))) break;
           tc_fence_after_sync();
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            mma_bf16_ss_pair(d, a_lo + s * (kABytes >> 4) + 2 * k, b_lo + s * (kBBytes >> 4) + 2 * k, kDescHi, kIdesc,
-                             (kb > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < kRowBytes / 32; ++k) {
+            // 32 bytes of K per instruction: 16 bf16 or 32 int8
+            const uint32_t a = a_lo + s * (kABytes >> 4) + 2 * k, b = b_lo + s * (kBBytes >> 4) + 2 * k;
+            if constexpr (kI8)
+              mma_i8_ss_pair(d, a, b, kDescHi, kIdesc, (kb > 0 || k > 0) ? 1u : 0u);
+            else
+              mma_bf16_ss_pair(d, a, b, kDescHi, kIdesc, (kb > 0 || k > 0) ? 1u : 0u);
+          }
           tc_commit_pair(empty(s));
           ++it;
         }
@@ -277,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = row < p.T;
       const uint32_t t_acc = tmem + lane_off + static_cast<uint32_t>(acc * kAccCols);
       __nv_bfloat16* dst = p.out + (row_ok ? row : 0) * p.out_stride;
+      const float row_scale = kI8 && row_ok ? __ldg(p.a_scale + row) : 1.0f;
       if constexpr (kEpi == kEpiSwiglu) {
         const int f0 = tc.n * kBoxRows;
 #pragma unroll 1
@@ -289,15 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; c += 8) {
               const int col = f0 + c0 + c;
               if (col < p.N) {
+                float gv[8], uv[8];
+                acc_values<kI8>(g + c, row_scale, p.w_scale + col, gv);
+                acc_values<kI8>(u + c, row_scale, p.w_scale + p.N + col, uv);
                 uint4 v;
-                v.x = pack_bf16x2(silu_mul(__uint_as_float(g[c]), __uint_as_float(u[c])),
-                                  silu_mul(__uint_as_float(g[c + 1]), __uint_as_float(u[c + 1])));
-                v.y = pack_bf16x2(silu_mul(__uint_as_float(g[c + 2]), __uint_as_float(u[c + 2])),
-                                  silu_mul(__uint_as_float(g[c + 3]), __uint_as_float(u[c + 3])));
-                v.z = pack_bf16x2(silu_mul(__uint_as_float(g[c + 4]), __uint_as_float(u[c + 4])),
-                                  silu_mul(__uint_as_float(g[c + 5]), __uint_as_float(u[c + 5])));
-                v.w = pack_bf16x2(silu_mul(__uint_as_float(g[c + 6]), __uint_as_float(u[c + 6])),
-                                  silu_mul(__uint_as_float(g[c + 7]), __uint_as_float(u[c + 7])));
+                v.x = pack_bf16x2(silu_mul(gv[0], uv[0]), silu_mul(gv[1], uv[1]));
+                v.y = pack_bf16x2(silu_mul(gv[2], uv[2]), silu_mul(gv[3], uv[3]));
+                v.z = pack_bf16x2(silu_mul(gv[4], uv[4]), silu_mul(gv[5], uv[5]));
+                v.w = pack_bf16x2(silu_mul(gv[6], uv[6]), silu_mul(gv[7], uv[7]));
                 *reinterpret_cast<uint4*>(dst + col) = v;
               }
             }
@@ -321,8 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int col = n0 + c0 + c;
               if (col < p.N) {
                 float o[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(y[c + e]);
+                acc_values<kI8>(y + c, row_scale, p.w_scale + col, o);
                 if constexpr (kEpi == kEpiGatedResidual) {
                   const uint4 xv = ld_nc16(xrow + col);
                   const float4 g0 = __ldg(reinterpret_cast<const float4*>(grow + col));
@@ -397,16 +429,19 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [rows, cols] bf16 with `stride` elements between rows, read as boxes of 64
-// columns x box_rows rows, 128-byte swizzled; reads past the edges give 0.
-bool make_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+// [rows, cols] bf16 (or, with i8, bytes) with `stride` elements between rows,
+// read as boxes of one 128-byte swizzle row x box_rows rows; reads past the
+// edges give 0.
+bool make_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int box_rows,
+                   bool i8) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
+  const int elem = i8 ? 1 : 2;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), static_cast<cuuint32_t>(box_rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * elem};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kRowBytes / elem), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+  return fn(map, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -415,24 +450,24 @@ bool make_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols
 // of CTA pairs that can be resident at once is queried on the first call
 // (which must precede any stream capture), so that the persistent grid never
 // leaves a pair waiting for a second wave.
-template <int kEpi>
+template <int kEpi, bool kI8>
 int resident_pairs(cudaLaunchConfig_t* cfg) {
   static int pairs[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
   if (pairs[dev] == 0) {
-    if (cudaFuncSetAttribute(linear_pair_kernel<kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(linear_pair_kernel<kEpi, kI8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Layout::kAlloc) != cudaSuccess)
       return -1;
     int n = 0;
     cfg->gridDim = dim3(2, 1, 1);
-    if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel<kEpi>, cfg) != cudaSuccess || n < 1) return -1;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel<kEpi, kI8>, cfg) != cudaSuccess || n < 1) return -1;
     pairs[dev] = n;
   }
   return pairs[dev];
 }
 
-template <int kEpi>
+template <int kEpi, bool kI8>
 int launch(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const Params& p,
            cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
@@ -446,12 +481,62 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int max_pairs = resident_pairs<kEpi>(&cfg);
+  const int max_pairs = resident_pairs<kEpi, kI8>(&cfg);
   if (max_pairs < 1) return -1;
   const int tiles = p.m_pairs * p.n_tiles;
   cfg.gridDim = dim3(2 * (tiles < max_pairs ? tiles : max_pairs), 1, 1);
-  if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<kEpi>, ta, tb0, tb1, p) != cudaSuccess) return -1;
+  if (cudaLaunchKernelEx(&cfg, linear_pair_kernel<kEpi, kI8>, ta, tb0, tb1, p) != cudaSuccess) return -1;
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <bool kI8>
+int launch_epi(int epi, const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const Params& p,
+               cudaStream_t stream) {
+  if (epi == kEpiGatedResidual) return launch<kEpiGatedResidual, kI8>(ta, tb0, tb1, p, stream);
+  if (epi == kEpiSwiglu) return launch<kEpiSwiglu, kI8>(ta, tb0, tb1, p, stream);
+  return launch<kEpiNone, kI8>(ta, tb0, tb1, p, stream);
+}
+
+// The launch with bf16 operands, or (a_scale, w_scale given) int8 ones; w_stride
+// elements between W's rows.
+int launch_rows(int epi, const void* a, int64_t a_stride, const float* a_scale, const void* w, int64_t w_stride,
+                const float* w_scale, const void* x, int64_t x_stride, const float* gate_res, const int32_t* cu,
+                int B, void* out, int64_t out_stride, int64_t T, int K, int N, int* status, long long timeout_ns,
+                cudaStream_t stream) {
+  const bool i8 = a_scale != nullptr;
+  CUtensorMap ta, tb0, tb1;
+  const bool swiglu = epi == kEpiSwiglu;
+  bool ok = make_rows_map(&ta, a, T, K, a_stride, kBM, i8);
+  if (swiglu) {
+    // W1 [2N, K]: gate rows [0, N) for the even CTA, up rows [N, 2N) for the
+    // odd one, each its own map so that rows past N read as zeros
+    const char* up = static_cast<const char*>(w) + static_cast<int64_t>(N) * w_stride * (i8 ? 1 : 2);
+    ok = ok && make_rows_map(&tb0, w, N, K, w_stride, kBoxRows, i8) &&
+         make_rows_map(&tb1, up, N, K, w_stride, kBoxRows, i8);
+  } else {
+    ok = ok && make_rows_map(&tb0, w, N, K, w_stride, kBoxRows, i8);
+    tb1 = tb0;
+  }
+  if (!ok) return -2;
+  const int block_k = i8 ? kRowBytes : kRowBytes / 2;
+  Params p;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.out_stride = out_stride;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.x_stride = x_stride;
+  p.gate_res = gate_res;
+  p.cu = cu;
+  p.a_scale = a_scale;
+  p.w_scale = w_scale;
+  p.B = B;
+  p.T = T;
+  p.N = N;
+  p.n_kb = (K + block_k - 1) / block_k;
+  p.m_pairs = static_cast<int>((T + 2 * kBM - 1) / (2 * kBM));
+  p.n_tiles = swiglu ? (N + kBoxRows - 1) / kBoxRows : (N + kAccCols - 1) / kAccCols;
+  p.status = status;
+  p.timeout_ns = timeout_ns;
+  return i8 ? launch_epi<true>(epi, ta, tb0, tb1, p, stream) : launch_epi<false>(epi, ta, tb0, tb1, p, stream);
 }
 
 }  // namespace
@@ -460,37 +545,17 @@ int launch_linear(int epi, const void* a, int64_t a_stride, const void* w, const
                   const float* gate_res, const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K,
                   int N, int* status, long long timeout_ns, cudaStream_t stream, int num_sms) {
   (void)num_sms;
-  CUtensorMap ta, tb0, tb1;
-  const bool swiglu = epi == kEpiSwiglu;
-  bool ok = make_rows_map(&ta, a, T, K, a_stride, kBM);
-  if (swiglu) {
-    // W1 [2N, K]: gate rows [0, N) for the even CTA, up rows [N, 2N) for the
-    // odd one, each its own map so that rows past N read as zeros
-    ok = ok && make_rows_map(&tb0, w, N, K, K, kBoxRows) &&
-         make_rows_map(&tb1, static_cast<const __nv_bfloat16*>(w) + static_cast<int64_t>(N) * K, N, K, K, kBoxRows);
-  } else {
-    ok = ok && make_rows_map(&tb0, w, N, K, K, kBoxRows);
-    tb1 = tb0;
-  }
-  if (!ok) return -2;
-  Params p;
-  p.out = static_cast<__nv_bfloat16*>(out);
-  p.out_stride = out_stride;
-  p.x = static_cast<const __nv_bfloat16*>(x);
-  p.x_stride = x_stride;
-  p.gate_res = gate_res;
-  p.cu = cu;
-  p.B = B;
-  p.T = T;
-  p.N = N;
-  p.n_kb = (K + kBK - 1) / kBK;
-  p.m_pairs = static_cast<int>((T + 2 * kBM - 1) / (2 * kBM));
-  p.n_tiles = swiglu ? (N + kBoxRows - 1) / kBoxRows : (N + kAccCols - 1) / kAccCols;
-  p.status = status;
-  p.timeout_ns = timeout_ns;
-  if (epi == kEpiGatedResidual) return launch<kEpiGatedResidual>(ta, tb0, tb1, p, stream);
-  if (swiglu) return launch<kEpiSwiglu>(ta, tb0, tb1, p, stream);
-  return launch<kEpiNone>(ta, tb0, tb1, p, stream);
+  return launch_rows(epi, a, a_stride, nullptr, w, K, nullptr, x, x_stride, gate_res, cu, B, out, out_stride, T, K, N,
+                     status, timeout_ns, stream);
+}
+
+int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_scale, const void* w8,
+                     int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride, const float* gate_res,
+                     const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K, int N, int* status,
+                     long long timeout_ns, cudaStream_t stream, int num_sms) {
+  (void)num_sms;
+  return launch_rows(epi, a8, a_stride, a_scale, w8, w_stride, w_scale, x, x_stride, gate_res, cu, B, out, out_stride,
+                     T, K, N, status, timeout_ns, stream);
 }
 
 }  // namespace pqk

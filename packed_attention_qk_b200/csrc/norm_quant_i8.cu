@@ -1,0 +1,301 @@
+// norm_quant_i8.cu -- gated residual, normalisation and adaLN modulation with
+// an int8 output and one scale per token: what modulate_swiglu writes as bf16,
+// in the form the int8 linear layers read, in one pass over the rows (the
+// pages fuse "residual connections", normalisation and modulation into fewer
+// launches: "FastH3 在八卡 B300 上实现完整 MP4 生成快于播放时长", section "融合 DiT
+// 算子"; that the layer behind reads 8-bit integers is a reading, not theirs).
+//
+//   x' = x + gate_res[s] * branch          (either may be left out)
+//   h  = norm(x') * weight * (1 + scale[s]) + shift[s]
+//   step = max_c |h_c| / 127 (1 for a zero row), code_c = rint(h_c / step)
+//
+// HBM-bound: x and branch are read once, x' and the codes written once (7
+// bytes an element with everything on). kTpr threads own one row and hold all
+// of it in registers as fp32, kCpt chunks of 8 elements a thread, so the three
+// dependent passes over a row (its moments, its largest |h|, its codes) cost
+// no memory traffic and h is never rounded before it is coded. Rows of one
+// warp need only shuffles; longer ones exchange one word per warp.
+//
+// Sums are fp32: at most 64 elements in a thread's chain, then a tree. The
+// largest |h| is taken on the bits (for non-negative floats their order is
+// the numbers', with NaN above infinity), so that a NaN cannot get lost in a
+// maximum: a row that is not finite gets scale NaN and codes 0, which makes
+// its dequantised values NaN, and no other row's.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pqk_internal.h"
+
+namespace pqk {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct NormQuantParams {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* branch;
+  __nv_bfloat16* x_out;
+  int8_t* h8;
+  float* h_scale;
+  int64_t x_stride, branch_stride, x_out_stride, h8_stride;
+  const __nv_bfloat16* weight;
+  const float* shift;
+  const float* scale;
+  const float* gate_res;
+  const int32_t* cu;
+  int B;
+  int64_t T;
+  int C;
+  int norm_type;
+  float eps;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Streamed once: kept out of L1, which the modulation vectors use.
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Request s with cu[s] <= t < cu[s+1] (the last such s when requests are
+// empty); always in 0..B-1, whatever cu holds.
+__device__ __forceinline__ int find_segment(const int32_t* cu, int B, int64_t t) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(__ldg(cu + mid)) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The kTpr threads of a row: combine one value of each and give every thread
+// the result. `slot`: kTpr / 32 words of shared memory used by this row only,
+// and by this exchange only until the row's next barrier.
+template <int kTpr, typename T, typename Op>
+__device__ __forceinline__ T row_reduce(T v, T* slot, int group, Op op) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, off));
+  if constexpr (kTpr > 32) {
+    const int warp_in_row = (threadIdx.x % kTpr) >> 5;
+    if ((threadIdx.x & 31) == 0) slot[warp_in_row] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kTpr) : "memory");
+    v = slot[0];
+#pragma unroll
+    for (int i = 1; i < kTpr / 32; ++i) v = op(v, slot[i]);
+  }
+  return v;
+}
+
+struct AddOp {
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
+struct MaxOp {
+  __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
+};
+
+template <int kTpr, int kCpt>
+__global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuantParams p) {
+  constexpr int kRows = kThreads / kTpr;
+  // one set of words for each of a row's exchanges, so that no exchange can
+  // overwrite words that a slow warp still reads
+  __shared__ float s_sum[kRows][2][kTpr / 32];
+  __shared__ uint32_t s_max[kRows][kTpr / 32];
+  const int group = threadIdx.x / kTpr;
+  const int lane = threadIdx.x % kTpr;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + group;
+  if (t >= p.T) return;  // a whole row's threads leave together: barriers count one row's threads
+  const int nchunks = p.C >> 3;
+  const int64_t mod_row = p.cu != nullptr ? static_cast<int64_t>(find_segment(p.cu, p.B, t)) * p.C : 0;
+
+  float v[kCpt][8];
+  {
+    uint4 xr[kCpt], br[kCpt];
+#pragma unroll
+    for (int i = 0; i < kCpt; ++i) {
+      const int c = lane + i * kTpr;
+      xr[i] = c < nchunks ? ld_stream16(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+    if (p.branch != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kCpt; ++i) {
+        const int c = lane + i * kTpr;
+        br[i] = c < nchunks ? ld_stream16(p.branch + t * p.branch_stride + c * 8) : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCpt; ++i) {
+      const int c = lane + i * kTpr;
+      unpack8(xr[i], v[i]);
+      if (p.branch != nullptr && c < nchunks) {
+        float b[8], g[8];
+        unpack8(br[i], b);
+        if (p.gate_res != nullptr) {
+          load8f(p.gate_res + mod_row + c * 8, g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] = fmaf(g[e], b[e], v[i][e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] += b[e];
+        }
+      }
+    }
+  }
+  // x' of every element is formed by the thread that read the element: x_out
+  // may be x (or branch) itself
+  if (p.x_out != nullptr) {
+#pragma unroll
+    for (int i = 0; i < kCpt; ++i) {
+      const int c = lane + i * kTpr;
+      if (c < nchunks) {
+        uint4 o;
+        o.x = pack_bf16x2(v[i][0], v[i][1]);
+        o.y = pack_bf16x2(v[i][2], v[i][3]);
+        o.z = pack_bf16x2(v[i][4], v[i][5]);
+        o.w = pack_bf16x2(v[i][6], v[i][7]);
+        *reinterpret_cast<uint4*>(p.x_out + t * p.x_out_stride + c * 8) = o;
+      }
+    }
+  }
+
+  const float inv_c = 1.0f / static_cast<float>(p.C);
+  if (p.norm_type != 2) {
+    float mu = 0.f;
+    if (p.norm_type == 1) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCpt; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[i][e];
+      mu = row_reduce<kTpr>(s, s_sum[group][0], group, AddOp()) * inv_c;
+    }
+    // centred second moment (mu = 0 for RMS); elements past C stay 0
+    float s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCpt; ++i) {
+      if (lane + i * kTpr < nchunks) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[i][e] -= mu;
+          s2 = fmaf(v[i][e], v[i][e], s2);
+        }
+      }
+    }
+    s2 = row_reduce<kTpr>(s2, s_sum[group][1], group, AddOp()) * inv_c;
+    // squares past fp32's range: the row counts as not finite
+    const float inv = s2 <= 3.402823466e38f ? 1.0f / sqrtf(s2 + p.eps) : __int_as_float(0x7fffffff);
+#pragma unroll
+    for (int i = 0; i < kCpt; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= inv;
+  }
+  uint32_t top = 0;  // bits of the largest |h|
+#pragma unroll
+  for (int i = 0; i < kCpt; ++i) {
+    const int c = lane + i * kTpr;
+    if (c < nchunks) {
+      if (p.weight != nullptr) {
+        float w[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight + c * 8)), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
+      }
+      if (p.shift != nullptr) {
+        float sc[8], sh[8];
+        load8f(p.scale + mod_row + c * 8, sc);
+        load8f(p.shift + mod_row + c * 8, sh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = fmaf(v[i][e], 1.0f + sc[e], sh[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
+    }
+  }
+  top = row_reduce<kTpr>(top, s_max[group], group, MaxOp());
+
+  const bool finite = top < 0x7f800000u;
+  const float amax = __uint_as_float(top);
+  // 127 / amax overflows below 2^-121: such rows are coded from h * 2^64
+  const float up = amax < 7.888609052e-31f ? 18446744073709551616.0f : 1.0f;
+  const float to_code = amax > 0.f ? 127.0f / (amax * up) : 0.f;
+  if (lane == 0) p.h_scale[t] = finite ? (amax > 0.f ? amax / 127.0f : 1.0f) : __int_as_float(0x7fffffff);
+#pragma unroll
+  for (int i = 0; i < kCpt; ++i) {
+    const int c = lane + i * kTpr;
+    if (c < nchunks) {
+      // h * to_code + 1.5 * 2^23: the integer nearest to the product (ties to
+      // even, no rounding in between) is the sum's low byte
+      uint32_t q[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(fmaf(v[i][e] * up, to_code, 12582912.0f));
+      uint2 o;
+      o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+      o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+      if (!finite) o = make_uint2(0u, 0u);
+      *reinterpret_cast<uint2*>(p.h8 + t * p.h8_stride + c * 8) = o;
+    }
+  }
+}
+
+template <int kTpr, int kCpt>
+int launch(const NormQuantParams& p, cudaStream_t stream) {
+  constexpr int kRows = kThreads / kTpr;
+  const int64_t blocks = (p.T + kRows - 1) / kRows;
+  norm_quant_i8_kernel<kTpr, kCpt><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int launch_norm_quant_i8(const void* x, int64_t x_stride, const void* branch, int64_t branch_stride, void* x_out,
+                         int64_t x_out_stride, void* h8, int64_t h8_stride, float* h_scale, const void* weight,
+                         const float* shift, const float* scale, const float* gate_res, const int32_t* cu, int B,
+                         int64_t T, int C, int norm_type, float eps, cudaStream_t stream) {
+  NormQuantParams p;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.branch = static_cast<const __nv_bfloat16*>(branch);
+  p.x_out = static_cast<__nv_bfloat16*>(x_out);
+  p.h8 = static_cast<int8_t*>(h8);
+  p.h_scale = h_scale;
+  p.x_stride = x_stride;
+  p.branch_stride = branch_stride;
+  p.x_out_stride = x_out_stride;
+  p.h8_stride = h8_stride;
+  p.weight = static_cast<const __nv_bfloat16*>(weight);
+  p.shift = shift;
+  p.scale = scale;
+  p.gate_res = gate_res;
+  p.cu = cu;
+  p.B = B;
+  p.T = T;
+  p.C = C;
+  p.norm_type = norm_type;
+  p.eps = eps;
+  const int nchunks = C / 8;
+  if (nchunks <= 32 * 2) return launch<32, 2>(p, stream);
+  if (nchunks <= 32 * 8) return launch<32, 8>(p, stream);
+  if (nchunks <= 128 * 8) return launch<128, 8>(p, stream);
+  return launch<256, 8>(p, stream);
+}
+
+}  // namespace pqk

@@ -413,6 +413,126 @@ int pqk_linear_swiglu(const void* a, int64_t a_stride_t, const void* w1, void* a
   return rc == 0 ? PQK_OK : (rc == -2 ? PQK_ERR_INVALID_ARG : PQK_ERR_CUDA);
 }
 
+int pqk_norm_modulate_i8(const void* x, int64_t x_stride_t, const void* branch, int64_t branch_stride_t, void* x_out,
+                         int64_t x_out_stride_t, void* h8, int64_t h8_stride_t, float* h_scale, const void* weight,
+                         const float* shift, const float* scale, const float* gate_res, const int32_t* cu_seqlens,
+                         int B, int64_t T, int C, int norm_type, float eps, void* stream) {
+  if (T < 0 || T > INT32_MAX - 512 || C <= 0 || C % 8 || C > 16384 || !(eps > 0.f)) return PQK_ERR_INVALID_ARG;
+  if (norm_type != PQK_NORM_RMS && norm_type != PQK_NORM_LAYER && norm_type != PQK_NORM_NONE)
+    return PQK_ERR_INVALID_ARG;
+  if ((shift == nullptr) != (scale == nullptr) || (gate_res != nullptr && branch == nullptr))
+    return PQK_ERR_INVALID_ARG;
+  const bool vectors = shift != nullptr || gate_res != nullptr;
+  if (vectors && (cu_seqlens == nullptr || B < 1)) return PQK_ERR_INVALID_ARG;
+  if (x_stride_t < C || h8_stride_t < C || (branch && branch_stride_t < C) || (x_out && x_out_stride_t < C))
+    return PQK_ERR_INVALID_ARG;
+  if (T == 0) return PQK_OK;
+  if (!x || !h8 || !h_scale) return PQK_ERR_INVALID_ARG;
+  // in place needs the same layout on both sides
+  if ((x_out == x && x_out_stride_t != x_stride_t) ||
+      (x_out != nullptr && x_out == branch && x_out_stride_t != branch_stride_t))
+    return PQK_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(branch) || !aligned16(x_out) || !aligned16(h8) || !aligned16(weight) ||
+      !aligned16(shift) || !aligned16(scale) || !aligned16(gate_res) || (reinterpret_cast<uintptr_t>(h_scale) % 4) ||
+      (x_stride_t % 8) || (h8_stride_t % 8) || (branch && branch_stride_t % 8) || (x_out && x_out_stride_t % 8))
+    return PQK_ERR_MISALIGNED;
+  DeviceInfo* d = nullptr;
+  if (int rc = check_device(&d)) return rc;
+  return pqk::launch_norm_quant_i8(x, x_stride_t, branch, branch_stride_t, x_out, x_out_stride_t, h8, h8_stride_t,
+                                   h_scale, weight, shift, scale, gate_res, vectors ? cu_seqlens : nullptr, B, T, C,
+                                   norm_type, eps, static_cast<cudaStream_t>(stream))
+             ? PQK_ERR_CUDA
+             : PQK_OK;
+}
+
+int pqk_quantize_i8(const void* x, int64_t x_stride_t, int64_t T, int C, void* x8, int64_t x8_stride_t, float* scales,
+                    void* stream) {
+  return pqk_norm_modulate_i8(x, x_stride_t, nullptr, 0, nullptr, 0, x8, x8_stride_t, scales, nullptr, nullptr,
+                              nullptr, nullptr, nullptr, 0, T, C, PQK_NORM_NONE, 1.0f, stream);
+}
+
+// int32 sums of K products of codes, at most 128 * 128 each, must not overflow.
+constexpr int kMaxI8K = INT32_MAX / (128 * 128);
+
+int pqk_linear_i8_gated_residual(const void* a8, int64_t a8_stride_t, const float* a_scale, const void* w8,
+                                 int64_t w8_stride_n, const float* w_scale, const void* x, int64_t x_stride_t,
+                                 const float* gate_res, const int32_t* cu_seqlens, int B, void* out,
+                                 int64_t out_stride_t, int64_t T, int K, int N, void* stream) {
+  if (T < 0 || T > INT32_MAX - 256 || K < 8 || N < 8 || K % 8 || N % 8 || K > kMaxI8K) return PQK_ERR_INVALID_ARG;
+  if (!linear_tiles_fit(T, N)) return PQK_ERR_INVALID_ARG;
+  const bool residual = x != nullptr || gate_res != nullptr;
+  if (residual && (x == nullptr || gate_res == nullptr || cu_seqlens == nullptr || B < 1 || x_stride_t < N))
+    return PQK_ERR_INVALID_ARG;
+  if (a8_stride_t < K || w8_stride_n < K || out_stride_t < N) return PQK_ERR_INVALID_ARG;
+  if (T == 0) return PQK_OK;
+  if (!a8 || !a_scale || !w8 || !w_scale || !out) return PQK_ERR_INVALID_ARG;
+  if (out == x && out_stride_t != x_stride_t) return PQK_ERR_INVALID_ARG;
+  if (!aligned16(a8) || !aligned16(w8) || !aligned16(w_scale) || !aligned16(out) || !aligned16(x) ||
+      !aligned16(gate_res) || (reinterpret_cast<uintptr_t>(a_scale) % 4) || (a8_stride_t % 16) ||
+      (w8_stride_n % 16) || (out_stride_t % 8) || (residual && (x_stride_t % 8)))
+    return PQK_ERR_MISALIGNED;
+  DeviceInfo* d = nullptr;
+  if (int rc = check_device(&d)) return rc;
+  const int rc = pqk::launch_linear_i8(residual ? pqk::kEpiGatedResidual : pqk::kEpiNone, a8, a8_stride_t, a_scale,
+                                       w8, w8_stride_n, w_scale, x, x_stride_t, gate_res, cu_seqlens, B, out,
+                                       out_stride_t, T, K, N, d->status, g_timeout_ns.load(),
+                                       static_cast<cudaStream_t>(stream), d->num_sms);
+  return rc == 0 ? PQK_OK : (rc == -2 ? PQK_ERR_INVALID_ARG : PQK_ERR_CUDA);
+}
+
+int pqk_linear_i8_swiglu(const void* a8, int64_t a8_stride_t, const float* a_scale, const void* w8,
+                         int64_t w8_stride_n, const float* w_scale, void* act, int64_t act_stride_t, int64_t T, int K,
+                         int F, void* stream) {
+  if (T < 0 || T > INT32_MAX - 256 || K < 8 || F < 8 || K % 8 || F % 8 || K > kMaxI8K) return PQK_ERR_INVALID_ARG;
+  if (!linear_tiles_fit(T, F)) return PQK_ERR_INVALID_ARG;
+  if (a8_stride_t < K || w8_stride_n < K || act_stride_t < F) return PQK_ERR_INVALID_ARG;
+  if (T == 0) return PQK_OK;
+  if (!a8 || !a_scale || !w8 || !w_scale || !act) return PQK_ERR_INVALID_ARG;
+  if (!aligned16(a8) || !aligned16(w8) || !aligned16(w_scale) || !aligned16(act) ||
+      (reinterpret_cast<uintptr_t>(a_scale) % 4) || (a8_stride_t % 16) || (w8_stride_n % 16) || (act_stride_t % 8))
+    return PQK_ERR_MISALIGNED;
+  DeviceInfo* d = nullptr;
+  if (int rc = check_device(&d)) return rc;
+  const int rc = pqk::launch_linear_i8(pqk::kEpiSwiglu, a8, a8_stride_t, a_scale, w8, w8_stride_n, w_scale, nullptr, 0,
+                                       nullptr, nullptr, 0, act, act_stride_t, T, K, F, d->status,
+                                       g_timeout_ns.load(), static_cast<cudaStream_t>(stream), d->num_sms);
+  return rc == 0 ? PQK_OK : (rc == -2 ? PQK_ERR_INVALID_ARG : PQK_ERR_CUDA);
+}
+
+size_t pqk_varlen_cross_attn_workspace_size(int B, int D) {
+  return B < 1 || (D != 64 && D != 128) ? 0 : pqk::cross_attn_workspace_bytes(B, D);
+}
+
+int pqk_varlen_cross_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int64_t q_stride_t,
+                              int64_t k_stride_t, int64_t v_stride_t, int64_t o_stride_t,
+                              const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B, int64_t Tq, int64_t Tk,
+                              int H, int Hkv, int D, float softmax_scale, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (B < 1 || Tq < 0 || Tk < 0 || H <= 0 || Hkv <= 0 || H % Hkv || Tq > INT32_MAX - 512 || Tk > INT32_MAX - 512 ||
+      !(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
+    return PQK_ERR_INVALID_ARG;
+  if (!attn_tiles_fit(Tq, B, H)) return PQK_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return PQK_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(H) * D, kv_row = static_cast<int64_t>(Hkv) * D;
+  if (q_stride_t < row || o_stride_t < row || (Tk > 0 && (k_stride_t < kv_row || v_stride_t < kv_row)))
+    return PQK_ERR_INVALID_ARG;
+  if (Tq == 0) return PQK_OK;
+  if (!q || !o || !cu_seqlens_q || !cu_seqlens_k || (Tk > 0 && (!k || !v))) return PQK_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+      (reinterpret_cast<uintptr_t>(lse) % 4) || (q_stride_t % 8) || (o_stride_t % 8) ||
+      (Tk > 0 && (k_stride_t % 8 || v_stride_t % 8)))
+    return PQK_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < pqk_varlen_cross_attn_workspace_size(B, D)) return PQK_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return PQK_ERR_MISALIGNED;
+  DeviceInfo* d = nullptr;
+  if (int rc = check_device(&d)) return rc;
+  const int rc = pqk::launch_varlen_cross_attn(q, k, v, o, lse, q_stride_t, k_stride_t, v_stride_t, o_stride_t,
+                                               cu_seqlens_q, cu_seqlens_k, B, Tq, Tk, H, Hkv, D, softmax_scale,
+                                               workspace, d->status, g_timeout_ns.load(),
+                                               static_cast<cudaStream_t>(stream), d->num_sms);
+  return rc == 0 ? PQK_OK : (rc == -2 ? PQK_ERR_INVALID_ARG : PQK_ERR_CUDA);
+}
+
 int pqk_get_device_status(void* stream) {
   DeviceInfo* d = current_device();
   if (d == nullptr) return PQK_ERR_CUDA;

@@ -51,6 +51,20 @@ int launch_varlen_attn(const void* q, const void* k, const void* v, void* o, flo
                        float skip_tau = 0.0f, unsigned long long* skip_counts = nullptr,
                        const float* deq = nullptr, bool fp8_pv = false, bool cta_pairs = false);
 
+// Workspace of launch_varlen_cross_attn for B requests and head_dim D.
+size_t cross_attn_workspace_bytes(int B, int D);
+
+// Attention of the packed queries q [Tq, H, D] to the packed keys k, v
+// [Tk, Hkv, D] of the same request (cu_q, cu_k; query head h reads key head
+// h / (H / Hkv)): the schedule builder, the attention kernel and, when some
+// request's keys may have been cut into parts, the kernel that joins them.
+// Returns as launch_varlen_attn.
+int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* o, float* lse, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int64_t o_stride, const int32_t* cu_q,
+                             const int32_t* cu_k, int B, int64_t Tq, int64_t Tk, int H, int Hkv, int D,
+                             float softmax_scale, void* workspace, int* status, long long timeout_ns,
+                             cudaStream_t stream, int num_sms);
+
 // Per-head absmax e4m3 quantisation of Q and K ([T, H, D] bf16, strides in
 // elements) into q8, k8 ([T, H, D] bytes, contiguous). scales: [4H] floats,
 // [0, 2H) scratch (absmax bits), [2H, 4H) the dequantisation factors (Q's
@@ -75,6 +89,23 @@ constexpr int kEpiSwiglu = 2;         // out = silu(A W[:N]^T) * (A W[N:]^T), W 
 int launch_linear(int epi, const void* a, int64_t a_stride, const void* w, const void* x, int64_t x_stride,
                   const float* gate_res, const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K,
                   int N, int* status, long long timeout_ns, cudaStream_t stream, int num_sms);
+
+// launch_linear with signed 8-bit A and W (rows a_stride / w_stride bytes
+// apart, multiples of 16), a_scale [T] and w_scale [N] ([2N] for SwiGLU, the
+// gate rows' first) multiplying the exact int32 sums.
+int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_scale, const void* w8,
+                     int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride, const float* gate_res,
+                     const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K, int N, int* status,
+                     long long timeout_ns, cudaStream_t stream, int num_sms);
+
+// Gated residual, norm and modulation of [T, C] bf16 rows with an int8 output
+// and one scale per token. branch, x_out, weight, shift/scale, gate_res (a
+// branch is then added as it is) and cu (B requests; needed by the vectors
+// only) may be null; C <= 16384.
+int launch_norm_quant_i8(const void* x, int64_t x_stride, const void* branch, int64_t branch_stride, void* x_out,
+                         int64_t x_out_stride, void* h8, int64_t h8_stride, float* h_scale, const void* weight,
+                         const float* shift, const float* scale, const float* gate_res, const int32_t* cu, int B,
+                         int64_t T, int C, int norm_type, float eps, cudaStream_t stream);
 
 int launch_wait_selftest(int* status, long long timeout_ns, cudaStream_t stream);
 

@@ -128,6 +128,12 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Orders this thread's earlier shared-memory writes before reads of them by
+// the async proxy (an MMA's operand fetch) that a later hand-off allows.
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05
 
 // Allocates `ncols` tensor-memory columns (power of two >= 32) for this CTA
@@ -190,6 +196,23 @@ __device__ __forceinline__ void mma_f8_ss_w(uint32_t d_tmem, uint32_t a_lo, uint
       "mov.b64 da, {%1, %3};\n"
       "mov.b64 db, {%2, %3};\n"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %4, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D(tmem) (+)= A(smem) * B(smem), kind::i8 (signed 8-bit inputs, int32
+// accumulate, K = 32 per instruction), descriptors as (low, high) words.
+__device__ __forceinline__ void mma_i8_ss_w(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t desc_hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      ".reg .b64 da, db;\n"
+      "setp.ne.b32 p, %5, 0;\n"
+      "mov.b64 da, {%1, %3};\n"
+      "mov.b64 db, {%2, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], da, db, %4, p;\n"
       "}\n" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate)
       : "memory");
@@ -271,6 +294,12 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool b_mn_ma
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Instruction descriptor of kind::i8: int32 accumulator (bits 4-5 = 2), A and
+// B signed 8-bit integers (bits 7-9, 10-12 = 1), both K-major; no saturation.
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
 
 // Loads 32 consecutive 32-bit TMEM columns of this warp's 32 lanes (one
 // lane per thread) and waits for them, in one asm statement so no use of r[]
@@ -405,6 +434,21 @@ __device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint32_t a_lo,
       "mov.b64 da, {%1, %3};\n"
       "mov.b64 db, {%2, %3};\n"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, {%6, %6, %6, %6, %6, %6, %6, %6}, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate), "r"(0u)
+      : "memory");
+}
+// The pair form of mma_i8_ss_w.
+__device__ __forceinline__ void mma_i8_ss_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t desc_hi,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      ".reg .b64 da, db;\n"
+      "setp.ne.b32 p, %5, 0;\n"
+      "mov.b64 da, {%1, %3};\n"
+      "mov.b64 db, {%2, %3};\n"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], da, db, %4, {%6, %6, %6, %6, %6, %6, %6, %6}, p;\n"
       "}\n" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(desc_hi), "r"(idesc), "r"(accumulate), "r"(0u)
       : "memory");

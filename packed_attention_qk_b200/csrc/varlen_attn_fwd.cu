@@ -69,7 +69,18 @@
 // cluster barrier keeps the second CTA, whose copies signal the leader's
 // barriers, resident until then.
 //
-// Two compile-time variants of the same pipeline:
+// Cross-attention (kCross; bf16): the queries attend to another packed
+// sequence. A work unit has its own key range and key head; what else differs:
+//   - a unit of at most 128 query rows leaves the second query tile out, so
+//     that a few queries cost one product a key tile instead of two;
+//   - where there are fewer tiles than SMs, the keys of a tile are cut into
+//     parts, each a unit of its own that leaves its normalised fp32 rows and
+//     their log-sum-exp in the workspace for combine_parts_kernel;
+//   - V rows past a unit's last key are set to zero in shared memory before
+//     their product: they belong to another request, or to nobody, and a NaN
+//     or infinity there would survive the product with P = 0.
+//
+// Compile-time variants of the same pipeline:
 //   kSkip  block skipping ("Skip-Softmax", first page, bullet on TRTLLM_ATTN
 //          SAGE and Skip-Softmax): a softmax warp whose 32 rows all have the
 //          tile maximum more than skip_tau below their earlier maximum writes
@@ -171,6 +182,9 @@ struct AttnParams {
   float skip_tau;                        // block-skip threshold (log2 units), kSkip only
   const float* deq;                      // kFp8: [2H] dequantisation factors of Q's, then K's heads
   unsigned long long* skip_counts;       // nullable: [0] skipped warp blocks, [1] skipped O += P V products
+  int group;                             // kCross: query heads per key head
+  float* part_o;                         // kCross: [slots][kRowsPerWork][D] rows of cut tiles, and their
+  float* part_lse;                       // [slots][kRowsPerWork] log2-sum-exps
 };
 
 struct Work {
@@ -203,6 +217,89 @@ __device__ __forceinline__ Work decode_work(const int32_t* sched, int H, int w) 
   (void)H;
   return wk;
 }
+
+// Cross-attention: a unit's queries and keys. slot < 0: the unit holds all
+// keys of its tile and writes the outputs itself.
+struct CrossWork {
+  int head;
+  int kv_head;
+  int q0;
+  int q_end;    // one past the request's last query
+  int k_start;  // first key of the unit
+  int k_len;    // its keys (at least one)
+  int n_kv;
+  int slot;
+};
+
+// Schedule of a cross-attention call (int32): [0] units, [1] B, [2] the claim
+// counter, [3] tiles (256 queries x one head, requests with keys), [4] the
+// same of requests without keys, [5] key tiles per part (0: no tile is cut);
+// then, requests in schedule order, prefixes [B+1] of units, tiles and keyless
+// tiles, and q_start, q_len, k_start, k_len [B] each.
+constexpr int kCrossHeader = 8;
+__host__ __device__ constexpr size_t cross_sched_words(int B) {
+  return kCrossHeader + 3 * (static_cast<size_t>(B) + 1) + 4 * static_cast<size_t>(B);
+}
+struct CrossSched {
+  int32_t *unit_start, *tile_start, *empty_start, *q_start, *q_len, *k_start, *k_len;
+  __device__ __forceinline__ CrossSched(const int32_t* sched, int B) {
+    unit_start = const_cast<int32_t*>(sched) + kCrossHeader;
+    tile_start = unit_start + B + 1;
+    empty_start = tile_start + B + 1;
+    q_start = empty_start + B + 1;
+    q_len = q_start + B;
+    k_start = q_len + B;
+    k_len = k_start + B;
+  }
+};
+__device__ __forceinline__ int cross_parts(int n_kv, int part_tiles) {
+  return part_tiles == 0 ? 1 : (n_kv + part_tiles - 1) / part_tiles;
+}
+// The last r < B with start[r] <= i.
+__device__ __forceinline__ int find_last(const int32_t* start, int B, int i) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ CrossWork decode_cross(const int32_t* sched, int group, int w) {
+  const int B = sched[1];
+  const CrossSched cs(sched, B);
+  const int r = find_last(cs.unit_start, B, w);
+  const int local = w - cs.unit_start[r];
+  const int q_len = cs.q_len[r], k_len = cs.k_len[r];
+  const int all_kv = (k_len + kBN - 1) / kBN;
+  const int parts = cross_parts(all_kv, sched[5]);
+  const int part = local % parts;
+  const int tile = local / parts;
+  const int nqb = (q_len + kRowsPerWork - 1) / kRowsPerWork;
+  CrossWork wk;
+  wk.head = tile / nqb;
+  wk.kv_head = wk.head / group;
+  wk.q0 = cs.q_start[r] + (tile % nqb) * kRowsPerWork;
+  wk.q_end = cs.q_start[r] + q_len;
+  // parts of equal size to one key tile
+  const int first = static_cast<int>(static_cast<int64_t>(all_kv) * part / parts);
+  const int last = static_cast<int>(static_cast<int64_t>(all_kv) * (part + 1) / parts);
+  wk.k_start = cs.k_start[r] + first * kBN;
+  wk.k_len = min(last * kBN, k_len) - first * kBN;
+  wk.n_kv = last - first;
+  wk.slot = parts > 1 ? w : -1;
+  return wk;
+}
+
+// What the pipeline's roles ask of a unit of either kind.
+__device__ __forceinline__ int first_key(const Work& wk) { return wk.seg_start; }
+__device__ __forceinline__ int first_key(const CrossWork& wk) { return wk.k_start; }
+__device__ __forceinline__ int key_count(const Work& wk) { return wk.seg_len; }
+__device__ __forceinline__ int key_count(const CrossWork& wk) { return wk.k_len; }
+__device__ __forceinline__ int end_of_queries(const Work& wk) { return wk.seg_start + wk.seg_len; }
+__device__ __forceinline__ int end_of_queries(const CrossWork& wk) { return wk.q_end; }
+__device__ __forceinline__ int key_head(const Work& wk) { return wk.head; }
+__device__ __forceinline__ int key_head(const CrossWork& wk) { return wk.kv_head; }
 
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, int* status) {
   *abort_flag = 1;
@@ -243,16 +340,71 @@ constexpr int kSortLimit = 8192;  // requests ordered longest first up to this B
 // dynamic shared memory of the schedule kernel: one 64-bit sort key per request
 constexpr int kSchedSmem = kSortLimit * 8;
 
+// Fills sort_keys[0, B) with the requests of cu, longest first, ties by index
+// (the request in each key's low word): a bitonic sort of the keys
+// (INT32_MAX - length) << 32 | index over the next power of two, padded with
+// keys above every real one. By the whole block.
+__device__ __forceinline__ void sort_longest_first(const int32_t* cu, int B, uint64_t* sort_keys) {
+  int n = 1;
+  while (n < B) n <<= 1;
+  for (int i = threadIdx.x; i < n; i += kSchedThreads)
+    sort_keys[i] = i < B ? (static_cast<uint64_t>(static_cast<uint32_t>(INT32_MAX - (cu[i + 1] - cu[i]))) << 32) |
+                               static_cast<uint32_t>(i)
+                         : ~0ull;
+  __syncthreads();
+  for (int k = 2; k <= n; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = threadIdx.x; i < n; i += kSchedThreads) {
+        const int partner = i ^ j;
+        if (partner > i) {
+          const uint64_t a = sort_keys[i], b = sort_keys[partner];
+          if ((a > b) == ((i & k) == 0)) {
+            sort_keys[i] = b;
+            sort_keys[partner] = a;
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// out[i] = count(0) + ... + count(i - 1) for i < B; returns the total to every
+// thread. One chunk of kSchedThreads requests at a time (warp scans, then a
+// scan of warp sums). By the whole block.
+template <typename Count>
+__device__ __forceinline__ int32_t exclusive_prefix(int B, int32_t* out, Count count) {
+  __shared__ int32_t warp_sums[kSchedThreads / 32];
+  int32_t carry = 0;
+  for (int base = 0; base < B; base += kSchedThreads) {
+    const int i = base + threadIdx.x;
+    const int32_t n = i < B ? count(i) : 0;
+    int32_t incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, incl, off);
+      if ((threadIdx.x & 31) >= off) incl += y;
+    }
+    __syncthreads();  // the previous chunk's (or call's) sums have been read
+    if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = incl;
+    __syncthreads();
+    int32_t before = carry, all = carry;
+    for (int w = 0; w < kSchedThreads / 32; ++w) {
+      if (w < static_cast<int>(threadIdx.x >> 5)) before += warp_sums[w];
+      all += warp_sums[w];
+    }
+    if (i < B) out[i] = before + incl - n;
+    carry = all;
+  }
+  return carry;
+}
+
 __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int32_t* cu, int B, int64_t T, int H,
                                                                         int rows_per_work, int32_t* sched,
                                                                         int* status) {
   extern __shared__ uint64_t sort_keys[];
   __shared__ int bad;
-  __shared__ int32_t carry;
-  if (threadIdx.x == 0) {
-    bad = (cu[0] != 0 || static_cast<int64_t>(cu[B]) != T) ? 1 : 0;
-    carry = 0;
-  }
+  if (threadIdx.x == 0) bad = (cu[0] != 0 || static_cast<int64_t>(cu[B]) != T) ? 1 : 0;
   __syncthreads();
   for (int i = threadIdx.x; i < B; i += kSchedThreads)
     if (cu[i + 1] < cu[i]) bad = 1;
@@ -271,31 +423,7 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
     return;
   }
   if (B <= kSortLimit) {
-    // requests longest first, ties by index: a bitonic sort of the keys
-    // (INT32_MAX - length) << 32 | index over the next power of two, padded
-    // with keys above every real one
-    int n = 1;
-    while (n < B) n <<= 1;
-    for (int i = threadIdx.x; i < n; i += kSchedThreads)
-      sort_keys[i] = i < B ? (static_cast<uint64_t>(static_cast<uint32_t>(INT32_MAX - (cu[i + 1] - cu[i]))) << 32) |
-                                 static_cast<uint32_t>(i)
-                           : ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= n; k <<= 1) {
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        for (int i = threadIdx.x; i < n; i += kSchedThreads) {
-          const int partner = i ^ j;
-          if (partner > i) {
-            const uint64_t a = sort_keys[i], b = sort_keys[partner];
-            if ((a > b) == ((i & k) == 0)) {
-              sort_keys[i] = b;
-              sort_keys[partner] = a;
-            }
-          }
-        }
-        __syncthreads();
-      }
-    }
+    sort_longest_first(cu, B, sort_keys);
     for (int r = threadIdx.x; r < B; r += kSchedThreads) {
       const int i = static_cast<int>(sort_keys[r] & 0xffffffffu);
       seg_start[r] = cu[i];
@@ -309,33 +437,139 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
     }
   }
   __syncthreads();
-  // exclusive prefix of tiles per request in schedule order, one chunk of
-  // kSchedThreads requests at a time (warp scans, then a scan of warp sums)
-  __shared__ int32_t warp_sums[kSchedThreads / 32];
-  for (int base = 0; base < B; base += kSchedThreads) {
-    const int i = base + threadIdx.x;
-    const int32_t n = i < B ? ((seg_len[i] + rows_per_work - 1) / rows_per_work) * H : 0;
-    int32_t incl = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, incl, off);
-      if ((threadIdx.x & 31) >= off) incl += y;
-    }
-    if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = incl;
-    __syncthreads();
-    int32_t before = carry;
-    for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) before += warp_sums[w];
-    if (i < B) tile_start[i] = before + incl - n;
-    __syncthreads();
-    if (threadIdx.x == kSchedThreads - 1) carry = before + incl;
-    __syncthreads();
-  }
+  const int32_t total = exclusive_prefix(
+      B, tile_start, [&](int i) { return ((seg_len[i] + rows_per_work - 1) / rows_per_work) * H; });
   if (threadIdx.x == 0) {
-    tile_start[B] = carry;
-    sched[0] = carry;
+    tile_start[B] = total;
+    sched[0] = total;
     sched[1] = B;
     sched[2] = 0;  // claim counter
     sched[3] = rows_per_work;
+  }
+}
+
+// Tiles are cut along their keys when there are fewer of them than this (one
+// B200's SMs), into parts of at least kMinPartTiles key tiles, so that about
+// kCutUnits units of equal size result: at most twice as many.
+constexpr int kCutUnits = 148;
+constexpr int kMinPartTiles = 4;
+
+__global__ void __launch_bounds__(kSchedThreads)
+    build_cross_schedule_kernel(const int32_t* cu_q, const int32_t* cu_k, int B, int64_t Tq, int64_t Tk, int H,
+                                int32_t* sched, int* status) {
+  extern __shared__ uint64_t sort_keys[];
+  __shared__ int bad;
+  __shared__ unsigned long long key_tiles;  // of all tiles together
+  if (threadIdx.x == 0) {
+    bad = (cu_q[0] != 0 || cu_k[0] != 0 || static_cast<int64_t>(cu_q[B]) > Tq || static_cast<int64_t>(cu_k[B]) > Tk)
+              ? 1 : 0;
+    key_tiles = 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < B; i += kSchedThreads)
+    if (cu_q[i + 1] < cu_q[i] || cu_k[i + 1] < cu_k[i]) bad = 1;
+  __syncthreads();
+  if (bad) {
+    if (threadIdx.x < kCrossHeader) sched[threadIdx.x] = threadIdx.x == 1 ? B : 0;
+    if (threadIdx.x == 0) atomicCAS(status, 0, kStatusBadSeqlens);
+    return;
+  }
+  const CrossSched cs(sched, B);
+  const bool sorted = B <= kSortLimit;
+  if (sorted) sort_longest_first(cu_k, B, sort_keys);
+  for (int r = threadIdx.x; r < B; r += kSchedThreads) {
+    const int i = sorted ? static_cast<int>(sort_keys[r] & 0xffffffffu) : r;
+    cs.q_start[r] = cu_q[i];
+    cs.q_len[r] = cu_q[i + 1] - cu_q[i];
+    cs.k_start[r] = cu_k[i];
+    cs.k_len[r] = cu_k[i + 1] - cu_k[i];
+  }
+  __syncthreads();
+  auto tiles_of = [&](int r) { return (cs.q_len[r] + kRowsPerWork - 1) / kRowsPerWork * H; };
+  auto key_tiles_of = [&](int r) { return (cs.k_len[r] + kBN - 1) / kBN; };
+  const int32_t tiles = exclusive_prefix(B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
+  const int32_t empty = exclusive_prefix(B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
+  unsigned long long mine = 0;
+  for (int r = threadIdx.x; r < B; r += kSchedThreads)
+    mine += static_cast<unsigned long long>(tiles_of(r)) * key_tiles_of(r);
+  if (mine != 0) atomicAdd(&key_tiles, mine);
+  __syncthreads();
+  int part_tiles = 0;
+  if (tiles < kCutUnits) {
+    const unsigned long long even = (key_tiles + kCutUnits - 1) / kCutUnits;
+    part_tiles = even > kMinPartTiles ? static_cast<int>(even) : kMinPartTiles;
+  }
+  const int32_t units = exclusive_prefix(B, cs.unit_start, [&](int r) {
+    return cs.k_len[r] > 0 ? tiles_of(r) * cross_parts(key_tiles_of(r), part_tiles) : 0;
+  });
+  if (threadIdx.x == 0) {
+    cs.unit_start[B] = units;
+    cs.tile_start[B] = tiles;
+    cs.empty_start[B] = empty;
+    sched[0] = units;
+    sched[1] = B;
+    sched[2] = 0;  // claim counter
+    sched[3] = tiles;
+    sched[4] = empty;
+    sched[5] = part_tiles;
+    sched[6] = sched[7] = 0;
+  }
+}
+
+// The rows of cut tiles from their parts' rows o_i and log2-sum-exps u_i:
+// O = sum_i 2^(u_i - u) o_i / sum_i 2^(u_i - u) with u the largest u_i, and
+// lse = (u + log2 of that sum) ln 2. One warp a row, the parts in order.
+constexpr int kCombineThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_parts_kernel(const int32_t* sched, const float* part_o, const float* part_lse, __nv_bfloat16* o,
+                         float* lse, int64_t o_stride, int64_t Tq, int H) {
+  const int B = sched[1], tiles = sched[3], part_tiles = sched[5];
+  if (part_tiles == 0) return;
+  const CrossSched cs(sched, B);
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (kCombineThreads / 32);
+  // row-major over the tiles, so that tiles with few queries spread over the warps
+  for (int i = blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5); i < tiles * kRowsPerWork; i += warps) {
+    const int tile = i % tiles, row = i / tiles;
+    const int r = find_last(cs.tile_start, B, tile);
+    const int parts = cross_parts((cs.k_len[r] + kBN - 1) / kBN, part_tiles);
+    if (parts == 1) continue;
+    const int q_len = cs.q_len[r];
+    const int nqb = (q_len + kRowsPerWork - 1) / kRowsPerWork;
+    const int local = tile - cs.tile_start[r];
+    const int q_row = (local % nqb) * kRowsPerWork + row;
+    if (q_row >= q_len) continue;
+    const int64_t slot0 = cs.unit_start[r] + static_cast<int64_t>(local) * parts;
+    const float* u = part_lse + slot0 * kRowsPerWork + row;
+    const float* src = part_o + (slot0 * kRowsPerWork + row) * D + lane * (D / 32);
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, u[static_cast<int64_t>(k) * kRowsPerWork]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float sum = 0.f, acc[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float weight = ex2_approx(u[static_cast<int64_t>(k) * kRowsPerWork] - top);
+      sum += weight;
+      const float2* v = reinterpret_cast<const float2*>(src + static_cast<int64_t>(k) * kRowsPerWork * D);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        const float2 x = v[e];
+        acc[2 * e] = fmaf(weight, x.x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(weight, x.y, acc[2 * e + 1]);
+      }
+    }
+    const float inv = 1.0f / sum;
+    const int64_t t = cs.q_start[r] + q_row;
+    const int head = local / nqb;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(o + t * o_stride + head * D + lane * (D / 32));
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lse != nullptr && lane == 0)
+      lse[static_cast<int64_t>(head) * Tq + t] = (top + __log2f(sum)) * 0.69314718055994530942f;
   }
 }
 
@@ -441,7 +675,7 @@ __device__ __forceinline__ float exp_tile_store(const float (&s)[128], float sca
   return (l0 + l1) + (l2 + l3);
 }
 
-template <int D, bool kSkip, bool kFp8, bool kFp8Pv, bool kPair = false>
+template <int D, bool kSkip, bool kFp8, bool kFp8Pv, bool kPair = false, bool kCross = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
@@ -449,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(!kFp8 || D == 128, "FP8 Q K^T: one 128-byte swizzle row per token");
   static_assert(!kFp8Pv || kFp8, "FP8 P V comes with FP8 Q K^T");
   static_assert(!kPair || (D == 128 && !kSkip && !kFp8), "CTA pairs: bf16, head_dim 128, no block skipping");
+  static_assert(!kCross || (!kSkip && !kFp8 && !kPair), "cross-attention: bf16, one SM a unit, no block skipping");
   // FP8 Q K^T: the MMA thread waits for the next V stage (loaded long ago)
   // while it waits for P1 anyway, and probes the next K stage there without
   // blocking (its copy may still be in flight), instead of waiting for both
@@ -539,6 +774,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The index of this block's work tile wt, published by the producer in
   // slot wt % kWorkSlots (-1 once the list is exhausted); false when the
   // block aborts first.
+  auto decode = [&](int w) {
+    if constexpr (kCross) return decode_cross(p.sched, p.group, w); else return decode_work(p.sched, p.H, w);
+  };
+  // whether the unit has rows for the second query tile
+  auto two_tiles = [&](const auto& wk) { return !kCross || wk.q0 + kBM < end_of_queries(wk); };
   auto next_work = [&](int wt, int& w) {
     if (!mbar_wait(work_full(wt % kWorkSlots), (wt / kWorkSlots) & 1, abort_flag, p.timeout_ns)) return false;
     // on a pair's second CTA the slot was written by the leader's producer
@@ -619,10 +859,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         work_slot[wt % kWorkSlots] = w;
         mbar_arrive(work_full(wt % kWorkSlots));
         if (w < 0) break;
-        const Work wk = decode_work(p.sched, p.H, w);
-        mbar_arrive_expect_tx(q_full, 2 * kQKBytes);
+        const auto wk = decode(w);
+        const int n_q = two_tiles(wk) ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, n_q * kQKBytes);
         ++q_loads;
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < n_q; ++i) {
           if constexpr (kFp8) {
             tma_load_3d(q_smem + i * L::kTileBytes, &tm_q, q_full, 0, wk.head, wk.q0 + i * kBM);
           } else {
@@ -639,14 +880,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((kFp8 && kv == 0) || (kFp8Pv && kv == 1)) {
               // one 128-byte e4m3 row per token: a single 16 KB box
               mbar_arrive_expect_tx(kv_full(s), kQKBytes);
-              tma_load_3d(kv_smem + s * L::kStageBytes, kv == 0 ? &tm_k : &tm_v, kv_full(s), 0, wk.head,
-                          wk.seg_start + j * kBN);
+              tma_load_3d(kv_smem + s * L::kStageBytes, kv == 0 ? &tm_k : &tm_v, kv_full(s), 0, key_head(wk),
+                          first_key(wk) + j * kBN);
             } else {
               mbar_arrive_expect_tx(kv_full(s), L::kTileBytes);
               const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
               for (int sl = 0; sl < L::kSlabs; ++sl)
-                tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, tm, kv_full(s), sl * 64, wk.head,
-                            wk.seg_start + j * kBN);
+                tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, tm, kv_full(s), sl * 64, key_head(wk),
+                            first_key(wk) + j * kBN);
             }
             ++load_idx;
           }
@@ -675,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdescPV8 = idesc_e4m3_f32(kBM, D, true);
       uint32_t cons_idx = 0;
       uint32_t p_phase = 0;
+      uint32_t p_phase1 = 0;  // kCross: the second query tile's, which units with one tile pass by
       unsigned long long pv_skips = 0;
       // every softmax warp of group i voted to skip K/V tile j
       auto group_skips = [&](int i, int j) {
@@ -746,16 +988,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (;; ++wt) {
         int w;
         if (!(ok = next_work(wt, w)) || w < 0) break;
-        const Work wk = decode_work(p.sched, p.H, w);
-        const bool q1_in_request = wk.q0 + kBM < wk.seg_start + wk.seg_len;
+        const auto wk = decode(w);
+        const bool q1_in_request = wk.q0 + kBM < end_of_queries(wk);
+        const bool two = two_tiles(wk);
+        if constexpr (kCross) {
+          // A unit without a second query tile: that group's softmax warps
+          // arrive once when they have seen it, so that they cannot fall
+          // behind the ring of claimed units. Waited for before the unit's
+          // first product, so before the producer may claim the next unit:
+          // the group cannot arrive for that one before this wait is over.
+          if (!two) {
+            if (!(ok = mbar_wait(p_full(1), p_phase1, abort_flag, p.timeout_ns))) break;
+            p_phase1 ^= 1u;
+          }
+        }
         if (!(ok = mbar_wait(q_full, wt & 1, abort_flag, p.timeout_ns))) break;
         uint32_t k_stage_idx = cons_idx;
         if (!(ok = wait_stage(k_stage_idx))) break;
         tc_fence_after_sync();
         issue_qk(0, k_stage_idx % L::kStages);
         commit_all(s_full(0));
-        issue_qk(1, k_stage_idx % L::kStages);
-        commit_all(s_full(1));
+        if (two) {
+          issue_qk(1, k_stage_idx % L::kStages);
+          commit_all(s_full(1));
+        }
         commit_own(kv_empty(k_stage_idx % L::kStages));
         if (wk.n_kv == 1) commit_own(q_empty);
         ++cons_idx;
@@ -793,7 +1049,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             k_ready = j + 2 < wk.n_kv &&
                       mbar_test_wait(kv_full(next_nk % L::kStages), (next_nk / L::kStages) & 1);
           }
-          if (!(ok = mbar_wait(p_full(1), p_phase, abort_flag, p.timeout_ns))) break;
+          if constexpr (kCross) {
+            if (!two) {
+              commit_own(kv_empty(v_idx % L::kStages));
+              if (more) {
+                commit_own(kv_empty(nk_idx % L::kStages));
+                if (j + 2 == wk.n_kv) commit_own(q_empty);
+              }
+              p_phase ^= 1u;
+              v_idx = next_v;
+              nk_idx = next_nk;
+              continue;
+            }
+          }
+          if (!(ok = mbar_wait(p_full(1), kCross ? p_phase1 : p_phase, abort_flag, p.timeout_ns))) break;
           tc_fence_after_sync();
           if (kSkip && j > 0 && group_skips(1, j)) {
             if (q1_in_request) ++pv_skips;
@@ -809,6 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j + 2 == wk.n_kv) commit_own(q_empty);
           }
           p_phase ^= 1u;
+          p_phase1 ^= 1u;
           v_idx = next_v;
           nk_idx = next_nk;
         }
@@ -824,6 +1094,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = tmem + lane_off + (grp == 0 ? L::kTmemS0 : L::kTmemS1);
     const uint32_t t_o = tmem + lane_off + (grp == 0 ? L::kTmemO0 : L::kTmemO1);
     uint32_t s_phase = 0;
+    uint32_t o_phase = 0;      // kCross: this group's count of units, as a parity
+    uint32_t kv_idx = 0;       // kCross: index of the unit's first K copy
     int wt = 0;
     bool ok = true;
     unsigned long long warp_skips = 0;
@@ -831,7 +1103,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int w;
       ok = __all_sync(0xffffffffu, next_work(wt, w));
       if (!ok || w < 0) break;
-      const Work wk = decode_work(p.sched, p.H, w);
+      const auto wk = decode(w);
+      if constexpr (kCross) {
+        if (grp == 1 && !two_tiles(wk)) {
+          mbar_arrive(p_full(1));
+          continue;
+        }
+      }
       const int row = wk.q0 + static_cast<int>(rank) * kRowsPerWork + grp * kBM + r;
       // log2-domain score factor; FP8 scores carry the two heads' dequantisation factors
       const float sl2 = kFp8 ? p.scale_log2 * p.deq[wk.head] * p.deq[p.H + wk.head] : p.scale_log2;
@@ -843,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_phase ^= 1u;
         tc_fence_after_sync();
         // keys at or past the request end (last tile only) are masked
-        const int valid = j == wk.n_kv - 1 ? wk.seg_len - j * kBN : kBN;
+        const int valid = j == wk.n_kv - 1 ? key_count(wk) - j * kBN : kBN;
         float s[128];
         load_scores(t_s, valid, s);
         const float mx = row_max(s) * sl2;
@@ -852,7 +1130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // of the request has its tile maximum more than skip_tau below its
           // maximum over tiles 0..j-1. The vote goes to the MMA thread, which
           // leaves out O_i += P_i V_j when all four warps of the group drop it.
-          const bool in_request = row < wk.seg_start + wk.seg_len;
+          const bool in_request = row < end_of_queries(wk);
           const bool skip = __all_sync(0xffffffffu, !in_request || (j > 0 && mx < m_seen - p.skip_tau));
           m_seen = fmaxf(m_seen, mx);
           if (lane == 0) votes[(grp * 2 + (j & 1)) * 4 + (warp & 3)] = skip ? 1 : 0;
@@ -903,6 +1181,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l += exp_tile_store<kFp8Pv>(s, sl2, -m, t_s);
+        if constexpr (kCross) {
+          // V rows past the last key become zero before either group's
+          // product reads them (the first group's "P ready" precedes both)
+          if (grp == 0 && valid < kBN) {
+            const uint32_t idx = kv_idx + 2 * j + 1;
+            const int st = idx % L::kStages;
+            ok = __all_sync(0xffffffffu, mbar_wait(kv_full(st), (idx / L::kStages) & 1, abort_flag, p.timeout_ns));
+            if (!ok) break;
+            if (r >= valid) {
+#pragma unroll
+              for (int c = 0; c < L::kSlabs * 8; ++c)
+                *reinterpret_cast<uint4*>(smem + L::kKVOff + st * L::kStageBytes + (c / 8) * kSlabBytes + r * 128 +
+                                          (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+          }
+        }
         tc_fence_before_sync();
         if constexpr (kPair) {
           // one arrival per warp at the leader's barrier. P and the rescaled
@@ -921,12 +1216,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // epilogue: normalise O_i and write the valid rows
-      ok = __all_sync(0xffffffffu, mbar_wait(o_done(grp), wt & 1, abort_flag, p.timeout_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait(o_done(grp), kCross ? o_phase : wt & 1, abort_flag, p.timeout_ns));
       if (!ok) break;
+      o_phase ^= 1u;
+      kv_idx += 2 * wk.n_kv;
       tc_fence_after_sync();
       // FP8 P V accumulates V's codes: its dequantisation factor comes in here
       const float inv_l = (kFp8Pv ? p.deq[2 * p.H + wk.head] : 1.0f) / l;
-      const bool valid_row = row < wk.seg_start + wk.seg_len;
+      const bool valid_row = row < end_of_queries(wk);
+      if constexpr (kCross) {
+        if (wk.slot >= 0) {
+          const int64_t prow = static_cast<int64_t>(wk.slot) * kRowsPerWork + grp * kBM + r;
+          float4* part = reinterpret_cast<float4*>(p.part_o + prow * D);
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld_x32(t_o + c0, ov);
+            if (valid_row) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 4)
+                part[(c0 + c) / 4] = make_float4(__uint_as_float(ov[c]) * inv_l, __uint_as_float(ov[c + 1]) * inv_l,
+                                                 __uint_as_float(ov[c + 2]) * inv_l, __uint_as_float(ov[c + 3]) * inv_l);
+            }
+          }
+          if (valid_row) p.part_lse[prow] = m + __log2f(l);
+          tc_fence_before_sync();
+          continue;
+        }
+      }
       __nv_bfloat16* dst = p.o + static_cast<int64_t>(row) * p.o_stride + wk.head * D;
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
@@ -947,6 +1264,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (valid_row && p.lse != nullptr)
         p.lse[static_cast<int64_t>(wk.head) * p.T + row] = (m + __log2f(l)) * 0.69314718055994530942f;
       tc_fence_before_sync();
+    }
+    if constexpr (kCross) {
+      // queries without keys: O = 0, lse = -inf; tiles spread over the blocks
+      const int B = p.sched[1], n_empty = p.sched[4];
+      const CrossSched cs(p.sched, B);
+      for (int i = blockIdx.x; i < n_empty; i += gridDim.x) {
+        const int q = find_last(cs.empty_start, B, i);
+        const int nqb = (cs.q_len[q] + kRowsPerWork - 1) / kRowsPerWork;
+        const int local = i - cs.empty_start[q];
+        const int head = local / nqb;
+        const int in_request = (local % nqb) * kRowsPerWork + grp * kBM + r;
+        if (in_request < cs.q_len[q]) {
+          const int64_t t = cs.q_start[q] + in_request;
+          uint4* dst = reinterpret_cast<uint4*>(p.o + t * p.o_stride + head * D);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+          if (p.lse != nullptr) p.lse[static_cast<int64_t>(head) * p.T + t] = -INFINITY;
+        }
+      }
     }
     if (kSkip && p.skip_counts != nullptr && lane == 0 && warp_skips != 0) atomicAdd(&p.skip_counts[0], warp_skips);
     if (!ok) abort_all();
@@ -1046,12 +1382,14 @@ bool make_e4m3_map(CUtensorMap* map, const void* ptr, int64_t T, int H, int D, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool kCross>
 bool set_schedule_smem_attr() {
   static int done[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(build_schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedSmem) !=
+    if (cudaFuncSetAttribute(kCross ? reinterpret_cast<const void*>(build_cross_schedule_kernel)
+                                    : reinterpret_cast<const void*>(build_schedule_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedSmem) !=
         cudaSuccess)
       return false;
     done[dev] = 1;
@@ -1102,14 +1440,14 @@ int launch_attn_pair(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
-template <int D, bool kSkip, bool kFp8, bool kFp8Pv>
+template <int D, bool kSkip, bool kFp8, bool kFp8Pv, bool kCross = false>
 bool set_smem_attr() {
   static int done[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(attn_fwd_kernel<D, kSkip, kFp8, kFp8Pv>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<D>::kAlloc) != cudaSuccess)
+    if (cudaFuncSetAttribute(attn_fwd_kernel<D, kSkip, kFp8, kFp8Pv, false, kCross>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kAlloc) != cudaSuccess)
       return false;
     done[dev] = 1;
   }
@@ -1140,7 +1478,7 @@ int launch_varlen_attn(const void* q, const void* k, const void* v, void* o, flo
   int sort_n = 1;
   while (sort_n < B) sort_n <<= 1;
   const size_t sched_smem = B <= kSortLimit ? static_cast<size_t>(sort_n) * 8 : 0;
-  if (sched_smem > 48 * 1024 && !set_schedule_smem_attr()) return -1;
+  if (sched_smem > 48 * 1024 && !set_schedule_smem_attr<false>()) return -1;
   build_schedule_kernel<<<1, kSchedThreads, sched_smem, stream>>>(cu_seqlens, B, T, H, rows_per_work, sched,
                                                                   status);
   if (cudaGetLastError() != cudaSuccess) return -1;
@@ -1157,6 +1495,8 @@ int launch_varlen_attn(const void* q, const void* k, const void* v, void* o, flo
   p.skip_tau = skip_tau;
   p.skip_counts = skip_counts;
   p.deq = deq;
+  p.group = 1;
+  p.part_o = p.part_lse = nullptr;
   // upper bound of work tiles: every request adds at most one partial block
   const int64_t max_work = static_cast<int64_t>(H) * ((T + rows_per_work - 1) / rows_per_work + B);
   const int grid = static_cast<int>(max_work < num_sms ? max_work : num_sms);
@@ -1191,6 +1531,72 @@ int launch_varlen_attn(const void* q, const void* k, const void* v, void* o, flo
     attn_fwd_kernel<64, true, false, false><<<grid, kThreads, Layout<64>::kAlloc, stream>>>(tq, tk, tv, p);
   }
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+namespace {
+
+size_t cross_sched_bytes(int B) { return (cross_sched_words(B) * sizeof(int32_t) + 255) & ~static_cast<size_t>(255); }
+
+template <int D>
+int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, int grid,
+                 bool may_cut, cudaStream_t stream) {
+  if (!set_smem_attr<D, false, false, false, true>()) return -1;
+  attn_fwd_kernel<D, false, false, false, false, true><<<grid, kThreads, Layout<D>::kAlloc, stream>>>(tq, tk, tv, p);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  if (may_cut) {
+    combine_parts_kernel<D><<<2 * kCutUnits, kCombineThreads, 0, stream>>>(p.sched, p.part_o, p.part_lse, p.o, p.lse,
+                                                                           p.o_stride, p.T, p.H);
+    if (cudaGetLastError() != cudaSuccess) return -1;
+  }
+  return 0;
+}
+
+}  // namespace
+
+// The schedule, then the parts' rows and log2-sum-exps (at most twice
+// kCutUnits parts of kRowsPerWork rows).
+size_t cross_attn_workspace_bytes(int B, int D) {
+  return cross_sched_bytes(B) + static_cast<size_t>(2 * kCutUnits) * kRowsPerWork * (D + 1) * sizeof(float);
+}
+
+int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* o, float* lse, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, int64_t o_stride, const int32_t* cu_q,
+                             const int32_t* cu_k, int B, int64_t Tq, int64_t Tk, int H, int Hkv, int D,
+                             float softmax_scale, void* workspace, int* status, long long timeout_ns,
+                             cudaStream_t stream, int num_sms) {
+  CUtensorMap tq, tk, tv;
+  // without any key there is nothing to map: the maps are never read then
+  if (!make_qkv_map(&tq, q, Tq, H, D, q_stride)) return -2;
+  if (Tk > 0 ? !make_qkv_map(&tk, k, Tk, Hkv, D, k_stride) || !make_qkv_map(&tv, v, Tk, Hkv, D, v_stride) : false)
+    return -2;
+  if (Tk == 0) tk = tv = tq;
+  int32_t* sched = static_cast<int32_t*>(workspace);
+  int sort_n = 1;
+  while (sort_n < B) sort_n <<= 1;
+  const size_t sched_smem = B <= kSortLimit ? static_cast<size_t>(sort_n) * 8 : 0;
+  if (sched_smem > 48 * 1024 && !set_schedule_smem_attr<true>()) return -1;
+  build_cross_schedule_kernel<<<1, kSchedThreads, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H, sched, status);
+  if (cudaGetLastError() != cudaSuccess) return -1;
+  AttnParams p = {};
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.o_stride = o_stride;
+  p.T = Tq;
+  p.H = H;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.sched = sched;
+  p.status = status;
+  p.timeout_ns = timeout_ns;
+  p.group = H / Hkv;
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + cross_sched_bytes(B));
+  p.part_lse = p.part_o + static_cast<size_t>(2 * kCutUnits) * kRowsPerWork * D;
+  // no request has more than kMinPartTiles key tiles: no tile can be cut
+  const bool may_cut = Tk > static_cast<int64_t>(kMinPartTiles) * kBN;
+  const int64_t max_units = static_cast<int64_t>(H) * ((Tq + kRowsPerWork - 1) / kRowsPerWork + B) +
+                            (may_cut ? kCutUnits : 0);
+  const int grid = static_cast<int>(max_units < num_sms ? max_units : num_sms);
+  return D == 128 ? launch_cross<128>(tq, tk, tv, p, grid, may_cut, stream)
+                  : launch_cross<64>(tq, tk, tv, p, grid, may_cut, stream);
 }
 
 int launch_wait_selftest(int* status, long long timeout_ns, cudaStream_t stream) {

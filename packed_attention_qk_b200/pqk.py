@@ -26,6 +26,8 @@ EXPORTS = ("pqk_qk_norm_rope", "pqk_qk_norm_rope_e4m3", "pqk_qk_norm_rope_3axis"
            "pqk_varlen_attn_fwd_skip", "pqk_quantize_qk_e4m3", "pqk_varlen_attn_fwd_fp8qk", "pqk_quantize_e4m3",
            "pqk_varlen_attn_fwd_fp8",
            "pqk_varlen_attn_fwd_noalloc", "pqk_modulate_swiglu", "pqk_linear_gated_residual", "pqk_linear_swiglu",
+           "pqk_norm_modulate_i8", "pqk_quantize_i8", "pqk_linear_i8_gated_residual", "pqk_linear_i8_swiglu",
+           "pqk_varlen_cross_attn_workspace_size", "pqk_varlen_cross_attn_fwd",
            "pqk_get_device_status", "pqk_set_wait_timeout_ns", "pqk_set_attn_cta_pairs", "pqk_selftest_wait_timeout",
            "pqk_status_string",
            "pqk_version")
@@ -88,6 +90,21 @@ def lib(path: str | None = None) -> C.CDLL:
     L.pqk_linear_gated_residual.restype = i32
     L.pqk_linear_swiglu.argtypes = [vp, i64, vp, vp, i64, i64, i32, i32, vp]
     L.pqk_linear_swiglu.restype = i32
+    L.pqk_norm_modulate_i8.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32,
+                                       f32, vp]
+    L.pqk_norm_modulate_i8.restype = i32
+    L.pqk_quantize_i8.argtypes = [vp, i64, i64, i32, vp, i64, vp, vp]
+    L.pqk_quantize_i8.restype = i32
+    L.pqk_linear_i8_gated_residual.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, vp, vp, i32, vp, i64, i64, i32, i32,
+                                               vp]
+    L.pqk_linear_i8_gated_residual.restype = i32
+    L.pqk_linear_i8_swiglu.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, i32, i32, vp]
+    L.pqk_linear_i8_swiglu.restype = i32
+    L.pqk_varlen_cross_attn_workspace_size.argtypes = [i32, i32]
+    L.pqk_varlen_cross_attn_workspace_size.restype = sz
+    L.pqk_varlen_cross_attn_fwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, i32, i64, i64, i32, i32,
+                                            i32, f32, vp, sz, vp]
+    L.pqk_varlen_cross_attn_fwd.restype = i32
     L.pqk_get_device_status.argtypes = [vp]
     L.pqk_get_device_status.restype = i32
     L.pqk_set_wait_timeout_ns.argtypes = [i64]
@@ -133,6 +150,59 @@ def _token_stride(t, ndim: int) -> int:
             want *= t.shape[e]
         assert t.stride(d) == want, "only the token (first) dimension may be strided"
     return t.stride(0)
+
+
+class _Args:
+    """Checks of one call's tensors: type, shape, unit stride inside a row,
+    and the current CUDA device (the library launches on it)."""
+
+    def __init__(self, fn: str):
+        import torch
+        self.fn, self.torch, self.device = fn, torch, None
+
+    def fail(self, name: str, why: str):
+        raise ValueError(f"{self.fn}: {name} {why}")
+
+    def check(self, name: str, t, dtype: str, shape, *, rows: bool = False) -> int:
+        """t must be `dtype` of `shape` (None: any size), contiguous, or with
+        `rows` only contiguous inside a row (all dimensions but the first).
+        Returns the row stride."""
+        if not isinstance(t, self.torch.Tensor):
+            self.fail(name, "is not a tensor")
+        if t.dtype is not getattr(self.torch, dtype):
+            self.fail(name, f"is {t.dtype}, not {dtype}")
+        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            self.fail(name, f"has shape {tuple(t.shape)}, not {tuple('any' if w is None else w for w in shape)}")
+        if self.device is None:
+            if t.device.type != "cuda":
+                self.fail(name, f"is on {t.device}, not on a CUDA device")
+            if t.device.index != self.torch.cuda.current_device():
+                self.fail(name, f"is on {t.device}, not on the current device")
+            self.device = t.device
+        elif t.device != self.device:
+            self.fail(name, f"is on {t.device}, not on {self.device}")
+        want, strides, empty = 1, t.stride(), t.numel() == 0
+        for d in range(t.dim() - 1, 0, -1):
+            if strides[d] != want and t.shape[d] > 1 and not empty:
+                self.fail(name, f"is not contiguous inside a row (strides {strides})")
+            want *= t.shape[d]
+        if t.dim() == 1 and t.shape[0] > 1 and strides[0] != 1:
+            self.fail(name, "is not contiguous")
+        if t.dim() > 1 and t.shape[0] <= 1:
+            # the stride of one row (or none) means nothing: its length in whole 16-byte units
+            unit = 16 // t.element_size()
+            return -(-want // unit) * unit
+        if t.dim() > 1 and not rows and strides[0] != want:
+            self.fail(name, "is not contiguous")
+        return strides[0]
+
+
+def _rows_i8(T: int, C: int, device):
+    """An int8 [T, C] tensor whose rows start on 16-byte boundaries."""
+    import torch
+    wide = (C + 15) // 16 * 16
+    t = torch.empty((T, wide), dtype=torch.int8, device=device)
+    return t if wide == C else t[:, :C]
 
 
 # ---------------------------------------------------------------- calls
@@ -415,6 +485,153 @@ def linear_swiglu(a, w1, *, act=None, stream=None):
     _check("pqk_linear_swiglu", lib().pqk_linear_swiglu(
         _ptr(a), _token_stride(a, 2), _ptr(w1), _ptr(act), _token_stride(act, 2), T, K, F, _stream(stream)))
     return act
+
+
+def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, scale=None, cu_seqlens=None,
+                     norm_type: int = NORM_RMS, eps: float = 1e-6, x_out=None, h8=None, h_scale=None, stream=None):
+    """Gated residual + norm + adaLN modulation with an int8 output and one
+    scale per token: x' = x + gate_res[request] * branch (without gate_res:
+    x + branch), h = norm(x') * weight * (1 + scale[request]) +
+    shift[request], h8 = round(h / h_scale), h_scale = max |h| / 127.
+    x, branch, x_out: bf16 [T, C] (rows may be strided; x_out may be x);
+    weight bf16 [C]; gate_res, shift, scale fp32 [B, C]; cu_seqlens int32
+    [B+1]. Returns (x_out or None, h8 int8 [T, C], h_scale fp32 [T])."""
+    import torch
+    a = _Args("norm_modulate_i8")
+    x_stride = a.check("x", x, "bfloat16", (None, None), rows=True)
+    T, Cdim = x.shape
+    br_stride = xo_stride = 0
+    if branch is not None:
+        br_stride = a.check("branch", branch, "bfloat16", (T, Cdim), rows=True)
+    if x_out is not None:
+        xo_stride = a.check("x_out", x_out, "bfloat16", (T, Cdim), rows=True)
+    B = 0
+    if cu_seqlens is not None:
+        a.check("cu_seqlens", cu_seqlens, "int32", (None,))
+        B = cu_seqlens.shape[0] - 1
+    for name, t in (("gate_res", gate_res), ("shift", shift), ("scale", scale)):
+        if t is not None:
+            a.check(name, t, "float32", (B, Cdim))
+    if weight is not None:
+        a.check("weight", weight, "bfloat16", (Cdim,))
+    h8 = _rows_i8(T, Cdim, x.device) if h8 is None else h8
+    h_scale = torch.empty(T, dtype=torch.float32, device=x.device) if h_scale is None else h_scale
+    h8_stride = a.check("h8", h8, "int8", (T, Cdim), rows=True)
+    a.check("h_scale", h_scale, "float32", (T,))
+    _check("pqk_norm_modulate_i8", lib().pqk_norm_modulate_i8(
+        _ptr(x), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, _ptr(h8), h8_stride, _ptr(h_scale),
+        _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim, norm_type, eps,
+        _stream(stream)))
+    return x_out, h8, h_scale
+
+
+def quantize_i8(x, *, x8=None, scales=None, stream=None):
+    """The rows of a bf16 tensor [T, C] as int8 codes with one scale per row
+    (max |x| / 127). Returns (x8 int8 [T, C], scales fp32 [T])."""
+    import torch
+    a = _Args("quantize_i8")
+    x_stride = a.check("x", x, "bfloat16", (None, None), rows=True)
+    T, Cdim = x.shape
+    x8 = _rows_i8(T, Cdim, x.device) if x8 is None else x8
+    scales = torch.empty(T, dtype=torch.float32, device=x.device) if scales is None else scales
+    x8_stride = a.check("x8", x8, "int8", (T, Cdim), rows=True)
+    a.check("scales", scales, "float32", (T,))
+    _check("pqk_quantize_i8", lib().pqk_quantize_i8(_ptr(x), x_stride, T, Cdim, _ptr(x8), x8_stride, _ptr(scales),
+                                                     _stream(stream)))
+    return x8, scales
+
+
+def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None, cu_seqlens=None, out=None,
+                             stream=None):
+    """out = x + gate_res[request] * y with y = a_scale * w_scale * (a8 @
+    w8.T), the product in 8-bit integers; with x None y alone. a8: int8
+    [T, K], w8: int8 [N, K] (rows on 16-byte boundaries, as quantize_i8 and
+    norm_modulate_i8 give them), a_scale fp32 [T], w_scale fp32 [N], x bf16
+    [T, N], gate_res fp32 [B, N]. out (bf16) may be x (in place)."""
+    import torch
+    a = _Args("linear_i8_gated_residual")
+    a_stride = a.check("a8", a8, "int8", (None, None), rows=True)
+    T, K = a8.shape
+    w_stride = a.check("w8", w8, "int8", (None, K), rows=True)
+    N = w8.shape[0]
+    a.check("a_scale", a_scale, "float32", (T,))
+    a.check("w_scale", w_scale, "float32", (N,))
+    B = x_stride = 0
+    if cu_seqlens is not None:
+        a.check("cu_seqlens", cu_seqlens, "int32", (None,))
+        B = cu_seqlens.shape[0] - 1
+    if x is not None:
+        x_stride = a.check("x", x, "bfloat16", (T, N), rows=True)
+    if gate_res is not None:
+        a.check("gate_res", gate_res, "float32", (B, N))
+    out = torch.empty((T, N), dtype=torch.bfloat16, device=a8.device) if out is None else out
+    out_stride = a.check("out", out, "bfloat16", (T, N), rows=True)
+    _check("pqk_linear_i8_gated_residual", lib().pqk_linear_i8_gated_residual(
+        _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(x), x_stride, _ptr(gate_res),
+        _ptr(cu_seqlens), B, _ptr(out), out_stride, T, K, N, _stream(stream)))
+    return out
+
+
+def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
+    """act = silu(y[:, :F]) * y[:, F:] with y = a_scale * w_scale * (a8 @
+    w8.T), the product in 8-bit integers. a8: int8 [T, K], w8: int8 [2F, K],
+    a_scale fp32 [T], w_scale fp32 [2F]. Returns act bf16 [T, F]."""
+    import torch
+    a = _Args("linear_i8_swiglu")
+    a_stride = a.check("a8", a8, "int8", (None, None), rows=True)
+    T, K = a8.shape
+    w_stride = a.check("w8", w8, "int8", (None, K), rows=True)
+    F, odd = divmod(w8.shape[0], 2)
+    if odd:
+        a.fail("w8", "has an odd number of rows")
+    a.check("a_scale", a_scale, "float32", (T,))
+    a.check("w_scale", w_scale, "float32", (2 * F,))
+    act = torch.empty((T, F), dtype=torch.bfloat16, device=a8.device) if act is None else act
+    act_stride = a.check("act", act, "bfloat16", (T, F), rows=True)
+    _check("pqk_linear_i8_swiglu", lib().pqk_linear_i8_swiglu(
+        _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(act), act_stride, T, K, F,
+        _stream(stream)))
+    return act
+
+
+def varlen_cross_attn_workspace_size(B: int, D: int) -> int:
+    return int(lib().pqk_varlen_cross_attn_workspace_size(B, D))
+
+
+def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale: float | None = None, o=None,
+                          lse=None, workspace=None, want_lse: bool = False, stream=None):
+    """Packed attention of each request's queries to its own keys of another
+    packed sequence. q: bf16 [Tq, H, D]; k, v: bf16 [Tk, Hkv, D], Hkv a
+    divisor of H; cu_seqlens_q, cu_seqlens_k: int32 [B+1] on the device, from
+    0 to at most Tq and Tk (rows behind the last request are left as they
+    are). A request without keys gives o = 0, lse = -inf. Returns (o, lse
+    fp32 [H, Tq] or None)."""
+    import torch
+    a = _Args("varlen_cross_attn_fwd")
+    q_stride = a.check("q", q, "bfloat16", (None, None, None), rows=True)
+    Tq, H, D = q.shape
+    k_stride = a.check("k", k, "bfloat16", (None, None, D), rows=True)
+    Tk, Hkv = k.shape[:2]
+    v_stride = a.check("v", v, "bfloat16", (Tk, Hkv, D), rows=True)
+    a.check("cu_seqlens_q", cu_seqlens_q, "int32", (None,))
+    B = cu_seqlens_q.shape[0] - 1
+    a.check("cu_seqlens_k", cu_seqlens_k, "int32", (B + 1,))
+    scale = softmax_scale if softmax_scale is not None else D ** -0.5
+    o = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device) if o is None else o
+    o_stride = a.check("o", o, "bfloat16", (Tq, H, D), rows=True)
+    if lse is None and want_lse:
+        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        a.check("lse", lse, "float32", (H, Tq))
+    if workspace is None:
+        workspace = torch.empty(varlen_cross_attn_workspace_size(B, D), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.device != q.device:
+        a.fail("workspace", f"is not contiguous on {q.device}")
+    _check("pqk_varlen_cross_attn_fwd", lib().pqk_varlen_cross_attn_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), q_stride, k_stride, v_stride, o_stride, _ptr(cu_seqlens_q),
+        _ptr(cu_seqlens_k), B, Tq, Tk, H, Hkv, D, scale, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+    return o, lse
 
 
 def get_device_status(stream=None) -> int:
