@@ -549,11 +549,24 @@ int launch_linear(int epi, const void* a, int64_t a_stride, const void* w, const
                      status, timeout_ns, stream);
 }
 
+bool make_i8_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+  return make_rows_map(map, ptr, rows, cols, stride, box_rows, true);
+}
+
 int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_scale, const void* w8,
                      int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride, const float* gate_res,
                      const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K, int N, int* status,
                      long long timeout_ns, cudaStream_t stream, int num_sms) {
-  (void)num_sms;
+  const int n_kb = (K + kRowBytes - 1) / kRowBytes;
+  const int64_t pair_tiles = (T + 2 * kBM - 1) / (2 * kBM) * ((N + kAccCols - 1) / kAccCols);
+  if (pair_tiles <= num_sms / 4) {
+    const int token_tile = T <= 32 ? 32 : (T <= 64 ? 64 : 128);
+    const int64_t tiles = (T + token_tile - 1) / token_tile * ((N + 127) / 128) * (epi == kEpiSwiglu ? 2 : 1);
+    int split = 1;
+    while (split < 8 && 2 * split <= n_kb && tiles * split * 2 <= 2 * num_sms) split *= 2;
+    return launch_linear_i8_few(epi, a8, a_stride, a_scale, w8, w_stride, w_scale, x, x_stride, gate_res, cu, B, out,
+                                out_stride, T, K, N, token_tile, split, status, timeout_ns, stream);
+  }
   return launch_rows(epi, a8, a_stride, a_scale, w8, w_stride, w_scale, x, x_stride, gate_res, cu, B, out, out_stride,
                      T, K, N, status, timeout_ns, stream);
 }

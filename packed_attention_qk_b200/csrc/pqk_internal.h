@@ -98,6 +98,19 @@ int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_s
                      const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K, int N, int* status,
                      long long timeout_ns, cudaStream_t stream, int num_sms);
 
+// The same with W's rows as the MMA's M side and tiles of 32, 64 or 128 tokens,
+// the K range of a tile split over the CTAs of a cluster (1 to 8, at most the
+// number of 128-byte K blocks).
+int launch_linear_i8_few(int epi, const void* a8, int64_t a_stride, const float* a_scale, const void* w8,
+                         int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride,
+                         const float* gate_res, const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T,
+                         int K, int N, int token_tile, int split, int* status, long long timeout_ns,
+                         cudaStream_t stream);
+
+// Tensor map of [rows, cols] bytes, `stride` bytes between rows, read as boxes
+// of one 128-byte swizzle row x box_rows rows.
+bool make_i8_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int box_rows);
+
 // Gated residual, norm and modulation of [T, C] bf16 rows with an int8 output
 // and one scale per token. branch, x_out, weight, shift/scale, gate_res (a
 // branch is then added as it is) and cu (B requests; needed by the vectors

@@ -135,7 +135,7 @@ def _stream(stream) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t) -> int | None:
@@ -154,55 +154,109 @@ def _token_stride(t, ndim: int) -> int:
 
 class _Args:
     """Checks of one call's tensors: type, shape, unit stride inside a row,
-    and the current CUDA device (the library launches on it)."""
+    and the current CUDA device (the library launches on it). What a call
+    usually gets, a contiguous tensor of the right shape, passes in one
+    comparison: the checks of a call cost about as much as its launch."""
+
+    __slots__ = ("fn", "torch", "dev")
 
     def __init__(self, fn: str):
         import torch
-        self.fn, self.torch, self.device = fn, torch, None
+        self.fn, self.torch, self.dev = fn, torch, None
 
     def fail(self, name: str, why: str):
         raise ValueError(f"{self.fn}: {name} {why}")
 
-    def check(self, name: str, t, dtype: str, shape, *, rows: bool = False) -> int:
-        """t must be `dtype` of `shape` (None: any size), contiguous, or with
-        `rows` only contiguous inside a row (all dimensions but the first).
-        Returns the row stride."""
+    def first(self, name: str, t, dtype, ndim: int):
+        """The call's first tensor: its shape, once it is a CUDA tensor of the
+        current device with `ndim` dimensions."""
         if not isinstance(t, self.torch.Tensor):
             self.fail(name, "is not a tensor")
-        if t.dtype is not getattr(self.torch, dtype):
-            self.fail(name, f"is {t.dtype}, not {dtype}")
-        if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-            self.fail(name, f"has shape {tuple(t.shape)}, not {tuple('any' if w is None else w for w in shape)}")
-        if self.device is None:
-            if t.device.type != "cuda":
-                self.fail(name, f"is on {t.device}, not on a CUDA device")
-            if t.device.index != self.torch.cuda.current_device():
-                self.fail(name, f"is on {t.device}, not on the current device")
-            self.device = t.device
-        elif t.device != self.device:
-            self.fail(name, f"is on {t.device}, not on {self.device}")
-        want, strides, empty = 1, t.stride(), t.numel() == 0
-        for d in range(t.dim() - 1, 0, -1):
-            if strides[d] != want and t.shape[d] > 1 and not empty:
+        shape = t.shape
+        if t.dtype is not dtype:
+            self.fail(name, f"is {t.dtype}, not {str(dtype)[6:]}")
+        if len(shape) != ndim:
+            self.fail(name, f"has shape {tuple(shape)}, not {ndim} dimensions")
+        dev = t.get_device()
+        if dev < 0:
+            self.fail(name, f"is on {t.device}, not on a CUDA device")
+        if dev != self.torch.cuda.current_device():
+            self.fail(name, f"is on {t.device}, not on the current device")
+        self.dev = dev
+        return shape
+
+    def whole(self, name: str, t, dtype, shape) -> None:
+        """t must be `dtype`, of `shape` and contiguous."""
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == self.dev and t.is_contiguous():
+                return
+        except AttributeError:
+            self.fail(name, "is not a tensor")
+        self._kind(name, t, dtype, shape)
+        self.fail(name, f"is not contiguous (strides {t.stride()})")
+
+    def rows(self, name: str, t, dtype, shape) -> int:
+        """t must be `dtype`, of `shape` and contiguous inside a row (all
+        dimensions but the first). Returns the row stride; for at most one row,
+        whose stride means nothing, its length in whole 16-byte units."""
+        self._kind(name, t, dtype, shape)
+        strides = t.stride()
+        want = 1
+        for d in range(len(shape) - 1, 0, -1):
+            if strides[d] != want and shape[d] > 1 and t.numel() > 0:
                 self.fail(name, f"is not contiguous inside a row (strides {strides})")
-            want *= t.shape[d]
-        if t.dim() == 1 and t.shape[0] > 1 and strides[0] != 1:
-            self.fail(name, "is not contiguous")
-        if t.dim() > 1 and t.shape[0] <= 1:
-            # the stride of one row (or none) means nothing: its length in whole 16-byte units
+            want *= shape[d]
+        if shape[0] <= 1:
             unit = 16 // t.element_size()
             return -(-want // unit) * unit
-        if t.dim() > 1 and not rows and strides[0] != want:
-            self.fail(name, "is not contiguous")
         return strides[0]
 
+    def _kind(self, name: str, t, dtype, shape) -> None:
+        if not isinstance(t, self.torch.Tensor):
+            self.fail(name, "is not a tensor")
+        if t.dtype is not dtype:
+            self.fail(name, f"is {t.dtype}, not {str(dtype)[6:]}")
+        if t.shape != shape:
+            self.fail(name, f"has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.get_device() != self.dev:
+            self.fail(name, f"is on {t.device}, not on cuda:{self.dev}")
 
-def _rows_i8(T: int, C: int, device):
-    """An int8 [T, C] tensor whose rows start on 16-byte boundaries."""
-    import torch
+
+def _requests(a: _Args, cu_seqlens, name: str = "cu_seqlens") -> int:
+    """The number of requests of a cu_seqlens (0 for None)."""
+    if cu_seqlens is None:
+        return 0
+    if not isinstance(cu_seqlens, a.torch.Tensor) or cu_seqlens.dim() != 1:
+        a.fail(name, "is not a one-dimensional tensor")
+    n = cu_seqlens.shape[0]
+    a.whole(name, cu_seqlens, a.torch.int32, (n,))
+    return n - 1
+
+
+def _rows_i8(a: _Args, name: str, t, T: int, C: int, device):
+    """The int8 [T, C] tensor t, or a new one whose rows start on 16-byte
+    boundaries, and its row stride."""
+    if t is not None:
+        return t, a.rows(name, t, a.torch.int8, (T, C))
     wide = (C + 15) // 16 * 16
-    t = torch.empty((T, wide), dtype=torch.int8, device=device)
-    return t if wide == C else t[:, :C]
+    t = a.torch.empty((T, wide), dtype=a.torch.int8, device=device)
+    return (t if wide == C else t[:, :C]), wide
+
+
+def _floats(a: _Args, name: str, t, n: int, device):
+    """The fp32 [n] tensor t, or a new one."""
+    if t is None:
+        return a.torch.empty(n, dtype=a.torch.float32, device=device)
+    a.whole(name, t, a.torch.float32, (n,))
+    return t
+
+
+def _rows_bf16(a: _Args, name: str, t, shape, device):
+    """The bf16 tensor t of `shape`, or a new one, and its row stride."""
+    if t is not None:
+        return t, a.rows(name, t, a.torch.bfloat16, shape)
+    t = a.torch.empty(shape, dtype=a.torch.bfloat16, device=device)
+    return t, math.prod(shape[1:])
 
 
 # ---------------------------------------------------------------- calls
@@ -498,26 +552,23 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
     [B+1]. Returns (x_out or None, h8 int8 [T, C], h_scale fp32 [T])."""
     import torch
     a = _Args("norm_modulate_i8")
-    x_stride = a.check("x", x, "bfloat16", (None, None), rows=True)
-    T, Cdim = x.shape
-    br_stride = xo_stride = 0
-    if branch is not None:
-        br_stride = a.check("branch", branch, "bfloat16", (T, Cdim), rows=True)
-    if x_out is not None:
-        xo_stride = a.check("x_out", x_out, "bfloat16", (T, Cdim), rows=True)
-    B = 0
-    if cu_seqlens is not None:
-        a.check("cu_seqlens", cu_seqlens, "int32", (None,))
-        B = cu_seqlens.shape[0] - 1
-    for name, t in (("gate_res", gate_res), ("shift", shift), ("scale", scale)):
-        if t is not None:
-            a.check(name, t, "float32", (B, Cdim))
+    bf16, f32 = torch.bfloat16, torch.float32
+    shape = a.first("x", x, bf16, 2)
+    T, Cdim = shape
+    x_stride = a.rows("x", x, bf16, shape)
+    br_stride = 0 if branch is None else a.rows("branch", branch, bf16, shape)
+    xo_stride = 0 if x_out is None else a.rows("x_out", x_out, bf16, shape)
+    B = _requests(a, cu_seqlens)
+    if gate_res is not None:
+        a.whole("gate_res", gate_res, f32, (B, Cdim))
+    if shift is not None:
+        a.whole("shift", shift, f32, (B, Cdim))
+    if scale is not None:
+        a.whole("scale", scale, f32, (B, Cdim))
     if weight is not None:
-        a.check("weight", weight, "bfloat16", (Cdim,))
-    h8 = _rows_i8(T, Cdim, x.device) if h8 is None else h8
-    h_scale = torch.empty(T, dtype=torch.float32, device=x.device) if h_scale is None else h_scale
-    h8_stride = a.check("h8", h8, "int8", (T, Cdim), rows=True)
-    a.check("h_scale", h_scale, "float32", (T,))
+        a.whole("weight", weight, bf16, (Cdim,))
+    h8, h8_stride = _rows_i8(a, "h8", h8, T, Cdim, x.device)
+    h_scale = _floats(a, "h_scale", h_scale, T, x.device)
     _check("pqk_norm_modulate_i8", lib().pqk_norm_modulate_i8(
         _ptr(x), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, _ptr(h8), h8_stride, _ptr(h_scale),
         _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim, norm_type, eps,
@@ -530,15 +581,28 @@ def quantize_i8(x, *, x8=None, scales=None, stream=None):
     (max |x| / 127). Returns (x8 int8 [T, C], scales fp32 [T])."""
     import torch
     a = _Args("quantize_i8")
-    x_stride = a.check("x", x, "bfloat16", (None, None), rows=True)
-    T, Cdim = x.shape
-    x8 = _rows_i8(T, Cdim, x.device) if x8 is None else x8
-    scales = torch.empty(T, dtype=torch.float32, device=x.device) if scales is None else scales
-    x8_stride = a.check("x8", x8, "int8", (T, Cdim), rows=True)
-    a.check("scales", scales, "float32", (T,))
+    shape = a.first("x", x, torch.bfloat16, 2)
+    T, Cdim = shape
+    x_stride = a.rows("x", x, torch.bfloat16, shape)
+    x8, x8_stride = _rows_i8(a, "x8", x8, T, Cdim, x.device)
+    scales = _floats(a, "scales", scales, T, x.device)
     _check("pqk_quantize_i8", lib().pqk_quantize_i8(_ptr(x), x_stride, T, Cdim, _ptr(x8), x8_stride, _ptr(scales),
                                                      _stream(stream)))
     return x8, scales
+
+
+def _i8_operands(a: _Args, a8, a_scale, w8, w_scale):
+    i8, f32 = a.torch.int8, a.torch.float32
+    shape = a.first("a8", a8, i8, 2)
+    T, K = shape
+    a_stride = a.rows("a8", a8, i8, shape)
+    if not isinstance(w8, a.torch.Tensor) or w8.dim() != 2:
+        a.fail("w8", "is not a two-dimensional tensor")
+    N = w8.shape[0]
+    w_stride = a.rows("w8", w8, i8, (N, K))
+    a.whole("a_scale", a_scale, f32, (T,))
+    a.whole("w_scale", w_scale, f32, (N,))
+    return T, K, N, a_stride, w_stride
 
 
 def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None, cu_seqlens=None, out=None,
@@ -550,22 +614,12 @@ def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None,
     [T, N], gate_res fp32 [B, N]. out (bf16) may be x (in place)."""
     import torch
     a = _Args("linear_i8_gated_residual")
-    a_stride = a.check("a8", a8, "int8", (None, None), rows=True)
-    T, K = a8.shape
-    w_stride = a.check("w8", w8, "int8", (None, K), rows=True)
-    N = w8.shape[0]
-    a.check("a_scale", a_scale, "float32", (T,))
-    a.check("w_scale", w_scale, "float32", (N,))
-    B = x_stride = 0
-    if cu_seqlens is not None:
-        a.check("cu_seqlens", cu_seqlens, "int32", (None,))
-        B = cu_seqlens.shape[0] - 1
-    if x is not None:
-        x_stride = a.check("x", x, "bfloat16", (T, N), rows=True)
+    T, K, N, a_stride, w_stride = _i8_operands(a, a8, a_scale, w8, w_scale)
+    B = _requests(a, cu_seqlens)
+    x_stride = 0 if x is None else a.rows("x", x, torch.bfloat16, (T, N))
     if gate_res is not None:
-        a.check("gate_res", gate_res, "float32", (B, N))
-    out = torch.empty((T, N), dtype=torch.bfloat16, device=a8.device) if out is None else out
-    out_stride = a.check("out", out, "bfloat16", (T, N), rows=True)
+        a.whole("gate_res", gate_res, torch.float32, (B, N))
+    out, out_stride = _rows_bf16(a, "out", out, (T, N), a8.device)
     _check("pqk_linear_i8_gated_residual", lib().pqk_linear_i8_gated_residual(
         _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(x), x_stride, _ptr(gate_res),
         _ptr(cu_seqlens), B, _ptr(out), out_stride, T, K, N, _stream(stream)))
@@ -576,18 +630,12 @@ def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
     """act = silu(y[:, :F]) * y[:, F:] with y = a_scale * w_scale * (a8 @
     w8.T), the product in 8-bit integers. a8: int8 [T, K], w8: int8 [2F, K],
     a_scale fp32 [T], w_scale fp32 [2F]. Returns act bf16 [T, F]."""
-    import torch
     a = _Args("linear_i8_swiglu")
-    a_stride = a.check("a8", a8, "int8", (None, None), rows=True)
-    T, K = a8.shape
-    w_stride = a.check("w8", w8, "int8", (None, K), rows=True)
-    F, odd = divmod(w8.shape[0], 2)
+    T, K, rows, a_stride, w_stride = _i8_operands(a, a8, a_scale, w8, w_scale)
+    F, odd = divmod(rows, 2)
     if odd:
         a.fail("w8", "has an odd number of rows")
-    a.check("a_scale", a_scale, "float32", (T,))
-    a.check("w_scale", w_scale, "float32", (2 * F,))
-    act = torch.empty((T, F), dtype=torch.bfloat16, device=a8.device) if act is None else act
-    act_stride = a.check("act", act, "bfloat16", (T, F), rows=True)
+    act, act_stride = _rows_bf16(a, "act", act, (T, F), a8.device)
     _check("pqk_linear_i8_swiglu", lib().pqk_linear_i8_swiglu(
         _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(act), act_stride, T, K, F,
         _stream(stream)))
@@ -608,25 +656,29 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     fp32 [H, Tq] or None)."""
     import torch
     a = _Args("varlen_cross_attn_fwd")
-    q_stride = a.check("q", q, "bfloat16", (None, None, None), rows=True)
-    Tq, H, D = q.shape
-    k_stride = a.check("k", k, "bfloat16", (None, None, D), rows=True)
+    bf16 = torch.bfloat16
+    shape = a.first("q", q, bf16, 3)
+    Tq, H, D = shape
+    q_stride = a.rows("q", q, bf16, shape)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        a.fail("k", "is not a three-dimensional tensor")
     Tk, Hkv = k.shape[:2]
-    v_stride = a.check("v", v, "bfloat16", (Tk, Hkv, D), rows=True)
-    a.check("cu_seqlens_q", cu_seqlens_q, "int32", (None,))
-    B = cu_seqlens_q.shape[0] - 1
-    a.check("cu_seqlens_k", cu_seqlens_k, "int32", (B + 1,))
+    k_stride = a.rows("k", k, bf16, (Tk, Hkv, D))
+    v_stride = a.rows("v", v, bf16, (Tk, Hkv, D))
+    if cu_seqlens_q is None:
+        a.fail("cu_seqlens_q", "is not a one-dimensional tensor")
+    B = _requests(a, cu_seqlens_q, "cu_seqlens_q")
+    a.whole("cu_seqlens_k", cu_seqlens_k, torch.int32, (B + 1,))
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
-    o = torch.empty((Tq, H, D), dtype=q.dtype, device=q.device) if o is None else o
-    o_stride = a.check("o", o, "bfloat16", (Tq, H, D), rows=True)
-    if lse is None and want_lse:
-        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+    o, o_stride = _rows_bf16(a, "o", o, shape, q.device)
     if lse is not None:
-        a.check("lse", lse, "float32", (H, Tq))
+        a.whole("lse", lse, torch.float32, (H, Tq))
+    elif want_lse:
+        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = torch.empty(varlen_cross_attn_workspace_size(B, D), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous() or workspace.device != q.device:
-        a.fail("workspace", f"is not contiguous on {q.device}")
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != q.device:
+        a.fail("workspace", f"is not a contiguous tensor on {q.device}")
     _check("pqk_varlen_cross_attn_fwd", lib().pqk_varlen_cross_attn_fwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), q_stride, k_stride, v_stride, o_stride, _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), B, Tq, Tk, H, Hkv, D, scale, _ptr(workspace),
