@@ -567,7 +567,7 @@ PQK_API int pqk_linear_i8_swiglu(const void* a8, int64_t a8_stride_t, const floa
  *               pqk_varlen_cross_attn_workspace_size(B, D) bytes (0 for an
  *               unsupported B or D); contents need not be kept between calls,
  *               calls that may overlap on the GPU need one each.
- * D 64 or 128; (ceil(Tq/256) + B) * H below 2^31 - 2^20; Tq, Tk <= 2^31 - 513.
+ * D 64 or 128; (ceil(Tq/128) + B) * H at most 2^31 - 2^20; Tq, Tk <= 2^31 - 513.
  */
 PQK_API size_t pqk_varlen_cross_attn_workspace_size(int B, int D);
 PQK_API int pqk_varlen_cross_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse,

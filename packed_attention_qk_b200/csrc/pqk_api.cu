@@ -511,7 +511,9 @@ int pqk_varlen_cross_attn_fwd(const void* q, const void* k, const void* v, void*
   if (B < 1 || Tq < 0 || Tk < 0 || H <= 0 || Hkv <= 0 || H % Hkv || Tq > INT32_MAX - 512 || Tk > INT32_MAX - 512 ||
       !(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
     return PQK_ERR_INVALID_ARG;
-  if (!attn_tiles_fit(Tq, B, H)) return PQK_ERR_INVALID_ARG;
+  // its tiles have at least 128 rows (token x head) in use
+  if (((Tq + 127) / 128 + B) * static_cast<int64_t>(H) > static_cast<int64_t>(INT32_MAX) - (1 << 20))
+    return PQK_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return PQK_ERR_UNSUPPORTED;
   const int64_t row = static_cast<int64_t>(H) * D, kv_row = static_cast<int64_t>(Hkv) * D;
   if (q_stride_t < row || o_stride_t < row || (Tk > 0 && (k_stride_t < kv_row || v_stride_t < kv_row)))

@@ -71,14 +71,27 @@
 //
 // Cross-attention (kCross; bf16): the queries attend to another packed
 // sequence. A work unit has its own key range and key head; what else differs:
-//   - a unit of at most 128 query rows leaves the second query tile out, so
-//     that a few queries cost one product a key tile instead of two;
+//   - the query heads that share a key head share a unit: a query tile is
+//     128 / p.pack tokens x p.pack heads, so that K and V are read once for
+//     all of them (one box of the Q map; p.pack is 1 without shared heads);
+//   - a unit without rows for the second query tile leaves it out, so that a
+//     few queries cost one product a key tile instead of two;
 //   - where there are fewer tiles than SMs, the keys of a tile are cut into
 //     parts, each a unit of its own that leaves its normalised fp32 rows and
-//     their log-sum-exp in the workspace for combine_parts_kernel;
+//     their log-sum-exp in the workspace for combine_parts_kernel; in a part
+//     of a tile without second query tile the two softmax groups take turns
+//     on the key tiles (each with its own S, O and running maximum) and leave
+//     two such rows;
 //   - V rows past a unit's last key are set to zero in shared memory before
 //     their product: they belong to another request, or to nobody, and a NaN
-//     or infinity there would survive the product with P = 0.
+//     or infinity there would survive the product with P = 0;
+//   - the producer claims and decodes the next unit while the current one
+//     runs and hands the decoded unit to the other roles;
+//   - output rows go through shared memory, a warp's 32 rows x 128 bytes at a
+//     time, so that a store instruction covers 4 whole 128-byte lines instead
+//     of 16 bytes of 32 lines. With four key tiles a unit (512 text keys) the
+//     scattered stores took 220 of 790 us (55,296 queries x 512 keys, 40
+//     heads); with the 454 of a long self-attention they do not show.
 //
 // Compile-time variants of the same pipeline:
 //   kSkip  block skipping ("Skip-Softmax", first page, bullet on TRTLLM_ATTN
@@ -132,17 +145,19 @@ constexpr int kSlabBytes = 128 * 128;      // 128 rows x 64 bf16 (one 128-byte s
 // softmax warps: at most three slots are live.
 constexpr int kWorkSlots = 4;
 
-template <int D, bool kPair = false>
+template <int D, bool kPair = false, bool kCross = false>
 struct Layout {
   static constexpr int kSlabs = D / 64;
   static constexpr int kTileBytes = kSlabs * kSlabBytes;  // a Q tile; a whole K or V tile
   // a K/V stage: a whole tile, or on a CTA pair this CTA's half (64 keys of
   // K; 64 of V's columns for all 128 keys)
   static constexpr int kStageBytes = kPair ? kTileBytes / 2 : kTileBytes;
-  static constexpr int kStages = (kPair || D != 128) ? 10 : 5;
+  static constexpr int kStages = kCross ? (D == 128 ? 4 : 8) : ((kPair || D != 128) ? 10 : 5);
   static constexpr int kQOff = 0;
   static constexpr int kKVOff = 2 * kTileBytes;
-  static constexpr int kBarOff = kKVOff + kStages * kStageBytes;
+  // cross-attention: 32 output rows x 128 bytes for each softmax warp
+  static constexpr int kOutOff = kKVOff + kStages * kStageBytes;
+  static constexpr int kBarOff = kOutOff + (kCross ? 8 * 32 * 128 : 0);
   // barriers: kv_full[S], kv_empty[S], q_full, q_empty, s_full[2], p_full[2], o_done[2], drain,
   // work_full[kWorkSlots]
   static constexpr int kNumBars = 2 * kStages + 9 + kWorkSlots;
@@ -153,7 +168,9 @@ struct Layout {
   // claimed work-tile indices, a ring of kWorkSlots (-1: no more work)
   static constexpr int kWorkOff = kVoteOff + 16;
   // the producer's copy counts (K/V stages, Q pairs), left for the drain
-  static constexpr int kLoadsOff = kWorkOff + 4 * kWorkSlots;
+  // (kCross: the decoded units instead, eight words each)
+  static constexpr int kUnitOff = (kWorkOff + 15) / 16 * 16;
+  static constexpr int kLoadsOff = kCross ? kUnitOff + 32 * kWorkSlots : kWorkOff + 4 * kWorkSlots;
   static constexpr int kBytes = kLoadsOff + 8;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024
   static constexpr uint32_t kTmemS0 = 0, kTmemS1 = 128, kTmemO0 = 256, kTmemO1 = 256 + D;
@@ -182,6 +199,7 @@ struct AttnParams {
   float skip_tau;                        // block-skip threshold (log2 units), kSkip only
   const float* deq;                      // kFp8: [2H] dequantisation factors of Q's, then K's heads
   unsigned long long* skip_counts;       // nullable: [0] skipped warp blocks, [1] skipped O += P V products
+  int pack;                              // kCross: query heads per unit
   int group;                             // kCross: query heads per key head
   float* part_o;                         // kCross: [slots][kRowsPerWork][D] rows of cut tiles, and their
   float* part_lse;                       // [slots][kRowsPerWork] log2-sum-exps
@@ -218,11 +236,10 @@ __device__ __forceinline__ Work decode_work(const int32_t* sched, int H, int w) 
   return wk;
 }
 
-// Cross-attention: a unit's queries and keys. slot < 0: the unit holds all
-// keys of its tile and writes the outputs itself.
+// Cross-attention: a unit's queries and keys. slot < 0: the unit holds all keys of its tile and writes the
+// outputs itself.
 struct CrossWork {
-  int head;
-  int kv_head;
+  int head;     // first of its p.pack query heads; -1: no more work
   int q0;
   int q_end;    // one past the request's last query
   int k_start;  // first key of the unit
@@ -232,8 +249,8 @@ struct CrossWork {
 };
 
 // Schedule of a cross-attention call (int32): [0] units, [1] B, [2] the claim
-// counter, [3] tiles (256 queries x one head, requests with keys), [4] the
-// same of requests without keys, [5] key tiles per part (0: no tile is cut);
+// counter, [3] tiles (2 * (128 / pack) queries x pack heads, requests with
+// keys), [4] the same of requests without keys, [5] key tiles per part (0: no tile is cut);
 // then, requests in schedule order, prefixes [B+1] of units, tiles and keyless
 // tiles, and q_start, q_len, k_start, k_len [B] each.
 constexpr int kCrossHeader = 8;
@@ -265,7 +282,8 @@ __device__ __forceinline__ int find_last(const int32_t* start, int B, int i) {
   return lo;
 }
 
-__device__ __forceinline__ CrossWork decode_cross(const int32_t* sched, int group, int w) {
+// tile_tokens: queries of a whole tile (both query tiles).
+__device__ __forceinline__ CrossWork decode_cross(const int32_t* sched, int pack, int tile_tokens, int w) {
   const int B = sched[1];
   const CrossSched cs(sched, B);
   const int r = find_last(cs.unit_start, B, w);
@@ -275,17 +293,16 @@ __device__ __forceinline__ CrossWork decode_cross(const int32_t* sched, int grou
   const int parts = cross_parts(all_kv, sched[5]);
   const int part = local % parts;
   const int tile = local / parts;
-  const int nqb = (q_len + kRowsPerWork - 1) / kRowsPerWork;
+  const int nqb = (q_len + tile_tokens - 1) / tile_tokens;
   CrossWork wk;
-  wk.head = tile / nqb;
-  wk.kv_head = wk.head / group;
-  wk.q0 = cs.q_start[r] + (tile % nqb) * kRowsPerWork;
+  wk.head = tile / nqb * pack;
+  wk.q0 = cs.q_start[r] + (tile % nqb) * tile_tokens;
   wk.q_end = cs.q_start[r] + q_len;
   // parts of equal size to one key tile
-  const int first = static_cast<int>(static_cast<int64_t>(all_kv) * part / parts);
-  const int last = static_cast<int>(static_cast<int64_t>(all_kv) * (part + 1) / parts);
+  const int first = parts == 1 ? 0 : static_cast<int>(static_cast<int64_t>(all_kv) * part / parts);
+  const int last = parts == 1 ? all_kv : static_cast<int>(static_cast<int64_t>(all_kv) * (part + 1) / parts);
   wk.k_start = cs.k_start[r] + first * kBN;
-  wk.k_len = min(last * kBN, k_len) - first * kBN;
+  wk.k_len = (last < all_kv ? last * kBN : k_len) - first * kBN;
   wk.n_kv = last - first;
   wk.slot = parts > 1 ? w : -1;
   return wk;
@@ -298,8 +315,6 @@ __device__ __forceinline__ int key_count(const Work& wk) { return wk.seg_len; }
 __device__ __forceinline__ int key_count(const CrossWork& wk) { return wk.k_len; }
 __device__ __forceinline__ int end_of_queries(const Work& wk) { return wk.seg_start + wk.seg_len; }
 __device__ __forceinline__ int end_of_queries(const CrossWork& wk) { return wk.q_end; }
-__device__ __forceinline__ int key_head(const Work& wk) { return wk.head; }
-__device__ __forceinline__ int key_head(const CrossWork& wk) { return wk.kv_head; }
 
 __device__ __forceinline__ void raise_abort(volatile int* abort_flag, int* status) {
   *abort_flag = 1;
@@ -449,21 +464,24 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
 }
 
 // Tiles are cut along their keys when there are fewer of them than this (one
-// B200's SMs), into parts of at least kMinPartTiles key tiles, so that about
-// kCutUnits units of equal size result: at most twice as many.
+// B200's SMs): into parts of at most as many key tiles as make the units no
+// more than the SMs, but kMinPartTiles at least (a part costs its rows' way
+// through the workspace).
 constexpr int kCutUnits = 148;
 constexpr int kMinPartTiles = 4;
 
 __global__ void __launch_bounds__(kSchedThreads)
-    build_cross_schedule_kernel(const int32_t* cu_q, const int32_t* cu_k, int B, int64_t Tq, int64_t Tk, int H,
-                                int32_t* sched, int* status) {
+    build_cross_schedule_kernel(const int32_t* cu_q, const int32_t* cu_k, int B, int64_t Tq, int64_t Tk,
+                                int head_blocks, int tile_tokens, int32_t* sched, int* status) {
   extern __shared__ uint64_t sort_keys[];
   __shared__ int bad;
   __shared__ unsigned long long key_tiles;  // of all tiles together
+  __shared__ int most_tiles, count;
   if (threadIdx.x == 0) {
     bad = (cu_q[0] != 0 || cu_k[0] != 0 || static_cast<int64_t>(cu_q[B]) > Tq || static_cast<int64_t>(cu_k[B]) > Tk)
               ? 1 : 0;
     key_tiles = 0;
+    most_tiles = 0;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < B; i += kSchedThreads)
@@ -485,19 +503,38 @@ __global__ void __launch_bounds__(kSchedThreads)
     cs.k_len[r] = cu_k[i + 1] - cu_k[i];
   }
   __syncthreads();
-  auto tiles_of = [&](int r) { return (cs.q_len[r] + kRowsPerWork - 1) / kRowsPerWork * H; };
+  auto tiles_of = [&](int r) { return (cs.q_len[r] + tile_tokens - 1) / tile_tokens * head_blocks; };
   auto key_tiles_of = [&](int r) { return (cs.k_len[r] + kBN - 1) / kBN; };
   const int32_t tiles = exclusive_prefix(B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
   const int32_t empty = exclusive_prefix(B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
-  unsigned long long mine = 0;
-  for (int r = threadIdx.x; r < B; r += kSchedThreads)
-    mine += static_cast<unsigned long long>(tiles_of(r)) * key_tiles_of(r);
-  if (mine != 0) atomicAdd(&key_tiles, mine);
-  __syncthreads();
   int part_tiles = 0;
   if (tiles < kCutUnits) {
-    const unsigned long long even = (key_tiles + kCutUnits - 1) / kCutUnits;
-    part_tiles = even > kMinPartTiles ? static_cast<int>(even) : kMinPartTiles;
+    unsigned long long mine = 0;
+    int most = 0;
+    for (int r = threadIdx.x; r < B; r += kSchedThreads) {
+      const int kt = cs.q_len[r] > 0 ? key_tiles_of(r) : 0;
+      mine += static_cast<unsigned long long>(tiles_of(r)) * kt;
+      most = max(most, kt);
+    }
+    if (mine != 0) atomicAdd(&key_tiles, mine);
+    if (most != 0) atomicMax(&most_tiles, most);
+    __syncthreads();
+    // the least part size in [lo, hi] with at most kCutUnits units; hi cuts nothing
+    int hi = max(most_tiles, kMinPartTiles);
+    int lo = max(kMinPartTiles, static_cast<int>((key_tiles + kCutUnits - 1) / kCutUnits));
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      __syncthreads();
+      if (threadIdx.x == 0) count = 0;
+      __syncthreads();
+      int n = 0;
+      for (int r = threadIdx.x; r < B; r += kSchedThreads)
+        if (cs.k_len[r] > 0) n += tiles_of(r) * cross_parts(key_tiles_of(r), mid);
+      if (n != 0) atomicAdd(&count, n);
+      __syncthreads();
+      if (count <= kCutUnits) hi = mid; else lo = mid + 1;
+    }
+    part_tiles = hi;
   }
   const int32_t units = exclusive_prefix(B, cs.unit_start, [&](int r) {
     return cs.k_len[r] > 0 ? tiles_of(r) * cross_parts(key_tiles_of(r), part_tiles) : 0;
@@ -523,10 +560,11 @@ constexpr int kCombineThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_parts_kernel(const int32_t* sched, const float* part_o, const float* part_lse, __nv_bfloat16* o,
-                         float* lse, int64_t o_stride, int64_t Tq, int H) {
+                         float* lse, int64_t o_stride, int64_t Tq, int pack) {
   const int B = sched[1], tiles = sched[3], part_tiles = sched[5];
   if (part_tiles == 0) return;
   const CrossSched cs(sched, B);
+  const int tokens = kBM / pack;  // queries of one query tile
   const int lane = threadIdx.x & 31;
   const int warps = gridDim.x * (kCombineThreads / 32);
   // row-major over the tiles, so that tiles with few queries spread over the warps
@@ -536,25 +574,31 @@ __global__ void __launch_bounds__(kCombineThreads)
     const int parts = cross_parts((cs.k_len[r] + kBN - 1) / kBN, part_tiles);
     if (parts == 1) continue;
     const int q_len = cs.q_len[r];
-    const int nqb = (q_len + kRowsPerWork - 1) / kRowsPerWork;
+    const int nqb = (q_len + 2 * tokens - 1) / (2 * tokens);
     const int local = tile - cs.tile_start[r];
-    const int q_row = (local % nqb) * kRowsPerWork + row;
-    if (q_row >= q_len) continue;
-    const int64_t slot0 = cs.unit_start[r] + static_cast<int64_t>(local) * parts;
-    const float* u = part_lse + slot0 * kRowsPerWork + row;
-    const float* src = part_o + (slot0 * kRowsPerWork + row) * D + lane * (D / 32);
+    const int q_tile0 = (local % nqb) * 2 * tokens;
+    const int in_tile = row & (kBM - 1);
+    const int q_row = q_tile0 + (row >> 7) * tokens + in_tile / pack;
+    if (in_tile >= tokens * pack || q_row >= q_len) continue;
+    // rows of one query tile only: both softmax groups left some, 128 rows apart
+    const bool one = q_tile0 + tokens >= q_len;
+    const int n = one ? 2 * parts : parts;
+    const int64_t step = one ? kBM : kRowsPerWork;
+    const int64_t row0 = (cs.unit_start[r] + static_cast<int64_t>(local) * parts) * kRowsPerWork + row;
+    const float* u = part_lse + row0;
+    const float* src = part_o + row0 * D + lane * (D / 32);
     float top = -INFINITY;
-    for (int k = lane; k < parts; k += 32) top = fmaxf(top, u[static_cast<int64_t>(k) * kRowsPerWork]);
+    for (int k = lane; k < n; k += 32) top = fmaxf(top, u[k * step]);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float weight = ex2_approx(u[static_cast<int64_t>(k) * kRowsPerWork] - top);
+    for (int k = 0; k < n; ++k) {
+      const float weight = ex2_approx(u[k * step] - top);
       sum += weight;
-      const float2* v = reinterpret_cast<const float2*>(src + static_cast<int64_t>(k) * kRowsPerWork * D);
+      const float2* v = reinterpret_cast<const float2*>(src + k * step * D);
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) {
         const float2 x = v[e];
@@ -564,7 +608,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
     const float inv = 1.0f / sum;
     const int64_t t = cs.q_start[r] + q_row;
-    const int head = local / nqb;
+    const int head = local / nqb * pack + in_tile % pack;
     uint32_t* dst = reinterpret_cast<uint32_t*>(o + t * o_stride + head * D + lane * (D / 32));
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
@@ -679,7 +723,7 @@ template <int D, bool kSkip, bool kFp8, bool kFp8Pv, bool kPair = false, bool kC
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
-  using L = Layout<D, kPair>;
+  using L = Layout<D, kPair, kCross>;
   static_assert(!kFp8 || D == 128, "FP8 Q K^T: one 128-byte swizzle row per token");
   static_assert(!kFp8Pv || kFp8, "FP8 P V comes with FP8 Q K^T");
   static_assert(!kPair || (D == 128 && !kSkip && !kFp8), "CTA pairs: bf16, head_dim 128, no block skipping");
@@ -715,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_done = [&](int i) { return q_full + 48 + 8u * i; };
   const uint32_t drain = q_full + 64;
   auto work_full = [&](int i) { return q_full + 72 + 8u * i; };
-  volatile int* work_slot = reinterpret_cast<volatile int*>(smem + L::kWorkOff);
+  volatile int* work_slot = reinterpret_cast<volatile int*>(smem + (kCross ? L::kUnitOff : L::kWorkOff));
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbortOff);
   volatile uint8_t* votes = smem + L::kVoteOff;
@@ -774,18 +818,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The index of this block's work tile wt, published by the producer in
   // slot wt % kWorkSlots (-1 once the list is exhausted); false when the
   // block aborts first.
-  auto decode = [&](int w) {
-    if constexpr (kCross) return decode_cross(p.sched, p.group, w); else return decode_work(p.sched, p.H, w);
-  };
-  // whether the unit has rows for the second query tile
-  auto two_tiles = [&](const auto& wk) { return !kCross || wk.q0 + kBM < end_of_queries(wk); };
   auto next_work = [&](int wt, int& w) {
     if (!mbar_wait(work_full(wt % kWorkSlots), (wt / kWorkSlots) & 1, abort_flag, p.timeout_ns)) return false;
     // on a pair's second CTA the slot was written by the leader's producer
     if (kPair && !leader) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    w = work_slot[wt % kWorkSlots];
+    w = kCross ? work_slot[8 * (wt % kWorkSlots)] : work_slot[wt % kWorkSlots];
     return true;
   };
+  // Work tile w in full; cross-attention takes the producer's decoded copy,
+  // which stays in its slot until the unit kWorkSlots further on is handed over.
+  auto decode = [&](int wt, int w) {
+    if constexpr (kCross) {
+      const volatile int* src = work_slot + 8 * (wt % kWorkSlots);
+      CrossWork wk;
+      wk.head = src[0];
+      wk.q0 = src[1];
+      wk.q_end = src[2];
+      wk.k_start = src[3];
+      wk.k_len = src[4];
+      wk.n_kv = src[5];
+      wk.slot = src[6];
+      return wk;
+    } else {
+      return decode_work(p.sched, p.H, w);
+    }
+  };
+  // kCross: queries of one query tile; whether a unit has rows for the second
+  const int tile_q = kCross ? kBM / p.pack : kBM;
+  auto two_tiles = [&](const auto& wk) { return !kCross || wk.q0 + tile_q < end_of_queries(wk); };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------ TMA producer
@@ -850,6 +910,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      } else if constexpr (kCross) {
+        const uint32_t q_tile_bytes = static_cast<uint32_t>(L::kSlabs * 128 * tile_q * p.pack);
+        auto claim = [&]() {
+          const int w = atomicAdd(claim_counter, 1);
+          CrossWork wk = {};
+          wk.head = -1;
+          return w < n_work ? decode_cross(p.sched, p.pack, 2 * tile_q, w) : wk;
+        };
+        CrossWork wk = claim();
+        for (int wt = 0;; ++wt) {
+          // the Q tiles of the previous unit are no longer needed: hand over the next one
+          if (wt > 0 && !(ok = mbar_wait(q_empty, (wt - 1) & 1, abort_flag, p.timeout_ns))) break;
+          volatile int* dst = work_slot + 8 * (wt % kWorkSlots);
+          dst[0] = wk.head;
+          dst[1] = wk.q0;
+          dst[2] = wk.q_end;
+          dst[3] = wk.k_start;
+          dst[4] = wk.k_len;
+          dst[5] = wk.n_kv;
+          dst[6] = wk.slot;
+          mbar_arrive(work_full(wt % kWorkSlots));
+          if (wk.head < 0) break;
+          const int n_q = two_tiles(wk) ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, n_q * q_tile_bytes);
+          ++q_loads;
+          for (int i = 0; i < n_q; ++i)
+            for (int sl = 0; sl < L::kSlabs; ++sl)
+              tma_load_3d(q_smem + i * L::kTileBytes + sl * kSlabBytes, &tm_q, q_full, sl * 64, wk.head,
+                          wk.q0 + i * tile_q);
+          const int kv_head = wk.head / p.group;
+          for (int i = 0; i < 2 * wk.n_kv; ++i) {  // K_0, V_0, K_1, V_1, ...
+            const int s = load_idx % L::kStages;
+            const uint32_t round = load_idx / L::kStages;
+            if (round > 0 && !(ok = mbar_wait(kv_empty(s), (round - 1) & 1, abort_flag, p.timeout_ns))) break;
+            mbar_arrive_expect_tx(kv_full(s), L::kTileBytes);
+            const CUtensorMap* tm = (i & 1) == 0 ? &tm_k : &tm_v;
+            for (int sl = 0; sl < L::kSlabs; ++sl)
+              tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, tm, kv_full(s), sl * 64, kv_head,
+                          wk.k_start + (i >> 1) * kBN);
+            ++load_idx;
+          }
+          if (!ok) break;
+          wk = claim();  // while the unit's last key tiles are worked on
+        }
       } else {
       for (int wt = 0; ok; ++wt) {
         // the Q tiles of the previous work tile are no longer needed: claim the next one
@@ -859,11 +963,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         work_slot[wt % kWorkSlots] = w;
         mbar_arrive(work_full(wt % kWorkSlots));
         if (w < 0) break;
-        const auto wk = decode(w);
-        const int n_q = two_tiles(wk) ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, n_q * kQKBytes);
+        const Work wk = decode_work(p.sched, p.H, w);
+        mbar_arrive_expect_tx(q_full, 2 * kQKBytes);
         ++q_loads;
-        for (int i = 0; i < n_q; ++i) {
+        for (int i = 0; i < 2; ++i) {
           if constexpr (kFp8) {
             tma_load_3d(q_smem + i * L::kTileBytes, &tm_q, q_full, 0, wk.head, wk.q0 + i * kBM);
           } else {
@@ -880,14 +983,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((kFp8 && kv == 0) || (kFp8Pv && kv == 1)) {
               // one 128-byte e4m3 row per token: a single 16 KB box
               mbar_arrive_expect_tx(kv_full(s), kQKBytes);
-              tma_load_3d(kv_smem + s * L::kStageBytes, kv == 0 ? &tm_k : &tm_v, kv_full(s), 0, key_head(wk),
-                          first_key(wk) + j * kBN);
+              tma_load_3d(kv_smem + s * L::kStageBytes, kv == 0 ? &tm_k : &tm_v, kv_full(s), 0, wk.head,
+                          wk.seg_start + j * kBN);
             } else {
               mbar_arrive_expect_tx(kv_full(s), L::kTileBytes);
               const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
               for (int sl = 0; sl < L::kSlabs; ++sl)
-                tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, tm, kv_full(s), sl * 64, key_head(wk),
-                            first_key(wk) + j * kBN);
+                tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, tm, kv_full(s), sl * 64, wk.head,
+                            wk.seg_start + j * kBN);
             }
             ++load_idx;
           }
@@ -935,8 +1038,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t k_lo = smem_desc_lo(kv_smem, 16);
       const uint32_t v_lo = smem_desc_lo(kv_smem, kSlabBytes);
       // S_i = Q_i K^T over D/16 K-steps of 16 (32 bytes inside the 128-byte row)
-      auto issue_qk = [&](int i, int stage) {
-        const uint32_t a0 = q_lo + i * kTileWords;
+      auto issue_qk_of = [&](int i, int q_tile, int stage) {
+        const uint32_t a0 = q_lo + q_tile * kTileWords;
         const uint32_t b0 = k_lo + stage * kStageWords;
         if constexpr (kFp8) {
           // e4m3: K = 32 per instruction, 32 bytes inside the one 128-byte row
@@ -958,6 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
+      auto issue_qk = [&](int i, int stage) { issue_qk_of(i, i, stage); };
       // O_i (+)= P_i V over kBN/16 K-steps; V is MN-major: 64-wide column
       // slabs kSlabBytes apart, 8-row groups 1024 bytes apart
       auto issue_pv = [&](int i, int stage, bool accumulate) {
@@ -988,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (;; ++wt) {
         int w;
         if (!(ok = next_work(wt, w)) || w < 0) break;
-        const auto wk = decode(w);
+        const auto wk = decode(wt, w);
         const bool q1_in_request = wk.q0 + kBM < end_of_queries(wk);
         const bool two = two_tiles(wk);
         if constexpr (kCross) {
@@ -997,9 +1101,48 @@ __global__ void __launch_bounds__(kThreads, 1)
           // behind the ring of claimed units. Waited for before the unit's
           // first product, so before the producer may claim the next unit:
           // the group cannot arrive for that one before this wait is over.
-          if (!two) {
+          if (!two && wk.slot < 0) {
             if (!(ok = mbar_wait(p_full(1), p_phase1, abort_flag, p.timeout_ns))) break;
             p_phase1 ^= 1u;
+          }
+          // A part of a tile without second query tile: the groups take turns,
+          // group j % 2 on key tile j (there are at least two). The copies
+          // wanted at once, V_j to K_{j+2}, are at most four.
+          if (!two && wk.slot >= 0) {
+            if (!(ok = mbar_wait(q_full, wt & 1, abort_flag, p.timeout_ns))) break;
+            auto k_idx = [&](int j) { return cons_idx + 2 * j; };
+            for (int j = 0; j < 2 && ok; ++j) {
+              if (!(ok = wait_stage(k_idx(j)))) break;
+              tc_fence_after_sync();
+              issue_qk_of(j, 0, k_idx(j) % L::kStages);
+              commit_all(s_full(j));
+              commit_own(kv_empty(k_idx(j) % L::kStages));
+            }
+            if (!ok) break;
+            if (wk.n_kv == 2) commit_own(q_empty);
+            for (int j = 0; j < wk.n_kv; ++j) {
+              const int g = j & 1;
+              const bool more = j + 2 < wk.n_kv;
+              const uint32_t v_idx = k_idx(j) + 1, nk_idx = k_idx(j + 2);
+              if (!(ok = wait_stage(v_idx))) break;
+              if (more && !(ok = wait_stage(nk_idx))) break;
+              if (!(ok = mbar_wait(p_full(g), g == 0 ? p_phase : p_phase1, abort_flag, p.timeout_ns))) break;
+              if (g == 0) p_phase ^= 1u; else p_phase1 ^= 1u;
+              tc_fence_after_sync();
+              issue_pv(g, v_idx % L::kStages, j >= 2);
+              commit_own(kv_empty(v_idx % L::kStages));
+              if (more) {
+                issue_qk_of(g, 0, nk_idx % L::kStages);
+                commit_all(s_full(g));
+                commit_own(kv_empty(nk_idx % L::kStages));
+                if (j + 3 == wk.n_kv) commit_own(q_empty);
+              } else {
+                commit_all(o_done(g));
+              }
+            }
+            if (!ok) break;
+            cons_idx += 2 * wk.n_kv;
+            continue;
           }
         }
         if (!(ok = mbar_wait(q_full, wt & 1, abort_flag, p.timeout_ns))) break;
@@ -1103,25 +1246,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       int w;
       ok = __all_sync(0xffffffffu, next_work(wt, w));
       if (!ok || w < 0) break;
-      const auto wk = decode(w);
+      const auto wk = decode(wt, w);
+      // the groups take turns on the key tiles of a cut tile without second query tile
+      bool turns = false;
       if constexpr (kCross) {
-        if (grp == 1 && !two_tiles(wk)) {
+        turns = wk.slot >= 0 && !two_tiles(wk);
+        if (grp == 1 && !turns && !two_tiles(wk)) {
           mbar_arrive(p_full(1));
+          kv_idx += 2 * wk.n_kv;
           continue;
         }
       }
-      const int row = wk.q0 + static_cast<int>(rank) * kRowsPerWork + grp * kBM + r;
+      const int first_j = turns ? grp : 0, step_j = turns ? 2 : 1;
+      const int last_keys = key_count(wk) - (wk.n_kv - 1) * kBN;  // in the last key tile
+      const int row = kCross ? 0 : wk.q0 + static_cast<int>(rank) * kRowsPerWork + grp * kBM + r;
       // log2-domain score factor; FP8 scores carry the two heads' dequantisation factors
       const float sl2 = kFp8 ? p.scale_log2 * p.deq[wk.head] * p.deq[p.H + wk.head] : p.scale_log2;
       float m = -INFINITY, l = 0.f;
       float m_seen = -INFINITY;  // block skipping: running maximum over all earlier tiles
-      for (int j = 0; j < wk.n_kv; ++j) {
+      for (int j = first_j; j < wk.n_kv; j += step_j) {
         ok = __all_sync(0xffffffffu, mbar_wait(s_full(grp), s_phase, abort_flag, p.timeout_ns));
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after_sync();
         // keys at or past the request end (last tile only) are masked
-        const int valid = j == wk.n_kv - 1 ? key_count(wk) - j * kBN : kBN;
+        const int valid = j == wk.n_kv - 1 ? (kCross ? last_keys : key_count(wk) - j * kBN) : kBN;
         float s[128];
         load_scores(t_s, valid, s);
         const float mx = row_max(s) * sl2;
@@ -1154,9 +1303,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
         }
-        const bool need_rescale = j > 0 && mx > m + kRescaleThreshold;
+        const bool need_rescale = j >= step_j && mx > m + kRescaleThreshold;
         float alpha = 1.0f;
-        if (j == 0) {
+        if (j < step_j) {
           m = mx;
         } else if (need_rescale) {
           alpha = ex2_approx(m - mx);
@@ -1182,9 +1331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l += exp_tile_store<kFp8Pv>(s, sl2, -m, t_s);
         if constexpr (kCross) {
-          // V rows past the last key become zero before either group's
-          // product reads them (the first group's "P ready" precedes both)
-          if (grp == 0 && valid < kBN) {
+          // V rows past the last key become zero before any product reads
+          // them (the first group's "P ready" precedes both groups' products;
+          // when they take turns, the tile is this group's alone)
+          if ((grp == 0 || turns) && valid < kBN) {
             const uint32_t idx = kv_idx + 2 * j + 1;
             const int st = idx % L::kStages;
             ok = __all_sync(0xffffffffu, mbar_wait(kv_full(st), (idx / L::kStages) & 1, abort_flag, p.timeout_ns));
@@ -1225,8 +1375,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv_l = (kFp8Pv ? p.deq[2 * p.H + wk.head] : 1.0f) / l;
       const bool valid_row = row < end_of_queries(wk);
       if constexpr (kCross) {
-        if (wk.slot >= 0) {
-          const int64_t prow = static_cast<int64_t>(wk.slot) * kRowsPerWork + grp * kBM + r;
+        // the unit again from its slot: holding all of it through the loop
+        // over the key tiles cost spills
+        const auto un = decode(wt, w);
+        // this thread's token and head, of the query tile's tile_q x pack rows
+        const int r_token = r / p.pack;
+        const int q_row = un.q0 + (un.slot >= 0 && !two_tiles(un) ? 0 : grp * tile_q) + r_token;
+        const bool valid_row = r_token < tile_q && q_row < un.q_end;
+        if (un.slot >= 0) {
+          const int64_t prow = static_cast<int64_t>(un.slot) * kRowsPerWork + grp * kBM + r;
           float4* part = reinterpret_cast<float4*>(p.part_o + prow * D);
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -1243,6 +1400,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before_sync();
           continue;
         }
+        // 64 columns of the warp's 32 rows at a time: each lane puts its row's
+        // eight 16-byte pieces where no two lanes meet in a bank (piece ^ row
+        // in the row's 128 bytes), then eight lanes store one row
+        const int head = un.head + r - r_token * p.pack;
+        const uint64_t dst = reinterpret_cast<uint64_t>(
+            valid_row ? p.o + static_cast<int64_t>(q_row) * p.o_stride + head * D : nullptr);
+        uint8_t* stage = smem + L::kOutOff + warp * (32 * 128);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 64) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t ov[32];
+            tmem_ld_x32(t_o + c0 + half * 32, ov);
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+              uint4 v;
+              v.x = pack_bf16x2(__uint_as_float(ov[c]) * inv_l, __uint_as_float(ov[c + 1]) * inv_l);
+              v.y = pack_bf16x2(__uint_as_float(ov[c + 2]) * inv_l, __uint_as_float(ov[c + 3]) * inv_l);
+              v.z = pack_bf16x2(__uint_as_float(ov[c + 4]) * inv_l, __uint_as_float(ov[c + 5]) * inv_l);
+              v.w = pack_bf16x2(__uint_as_float(ov[c + 6]) * inv_l, __uint_as_float(ov[c + 7]) * inv_l);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((half * 4 + c / 8) ^ (lane & 7)) * 16)) = v;
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int srow = i * 4 + (lane >> 3), piece = lane & 7;
+            const uint64_t to = __shfl_sync(0xffffffffu, dst, srow);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + srow * 128 + ((piece ^ (srow & 7)) * 16));
+            if (to != 0) reinterpret_cast<uint4*>(to)[c0 / 8 + piece] = v;
+          }
+          __syncwarp();
+        }
+        if (valid_row && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(head) * p.T + q_row] = (m + __log2f(l)) * 0.69314718055994530942f;
+        tc_fence_before_sync();
+        continue;
       }
       __nv_bfloat16* dst = p.o + static_cast<int64_t>(row) * p.o_stride + wk.head * D;
 #pragma unroll
@@ -1271,11 +1465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CrossSched cs(p.sched, B);
       for (int i = blockIdx.x; i < n_empty; i += gridDim.x) {
         const int q = find_last(cs.empty_start, B, i);
-        const int nqb = (cs.q_len[q] + kRowsPerWork - 1) / kRowsPerWork;
+        const int nqb = (cs.q_len[q] + 2 * tile_q - 1) / (2 * tile_q);
         const int local = i - cs.empty_start[q];
-        const int head = local / nqb;
-        const int in_request = (local % nqb) * kRowsPerWork + grp * kBM + r;
-        if (in_request < cs.q_len[q]) {
+        const int r_token = r / p.pack;
+        const int head = local / nqb * p.pack + r - r_token * p.pack;
+        const int in_request = (local % nqb) * 2 * tile_q + grp * tile_q + r_token;
+        if (r_token < tile_q && in_request < cs.q_len[q]) {
           const int64_t t = cs.q_start[q] + in_request;
           uint4* dst = reinterpret_cast<uint4*>(p.o + t * p.o_stride + head * D);
 #pragma unroll
@@ -1355,13 +1550,15 @@ EncodeTiledFn encode_fn() {
 }
 
 // [T, H, D] bf16 with `stride` elements between tokens, read as boxes of
-// 64 columns x 1 head x box_rows tokens, 128-byte swizzled; rows past T read as 0.
-bool make_qkv_map(CUtensorMap* map, const void* ptr, int64_t T, int H, int D, int64_t stride, int box_rows = kBM) {
+// 64 columns x box_heads heads x box_rows tokens, 128-byte swizzled; rows past
+// T read as 0.
+bool make_qkv_map(CUtensorMap* map, const void* ptr, int64_t T, int H, int D, int64_t stride, int box_rows = kBM,
+                  int box_heads = 1) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1447,7 +1644,8 @@ bool set_smem_attr() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   if (!done[dev]) {
     if (cudaFuncSetAttribute(attn_fwd_kernel<D, kSkip, kFp8, kFp8Pv, false, kCross>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kAlloc) != cudaSuccess)
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<D, false, kCross>::kAlloc) != cudaSuccess)
       return false;
     done[dev] = 1;
   }
@@ -1495,7 +1693,7 @@ int launch_varlen_attn(const void* q, const void* k, const void* v, void* o, flo
   p.skip_tau = skip_tau;
   p.skip_counts = skip_counts;
   p.deq = deq;
-  p.group = 1;
+  p.pack = p.group = 1;
   p.part_o = p.part_lse = nullptr;
   // upper bound of work tiles: every request adds at most one partial block
   const int64_t max_work = static_cast<int64_t>(H) * ((T + rows_per_work - 1) / rows_per_work + B);
@@ -1541,11 +1739,12 @@ template <int D>
 int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, int grid,
                  bool may_cut, cudaStream_t stream) {
   if (!set_smem_attr<D, false, false, false, true>()) return -1;
-  attn_fwd_kernel<D, false, false, false, false, true><<<grid, kThreads, Layout<D>::kAlloc, stream>>>(tq, tk, tv, p);
+  attn_fwd_kernel<D, false, false, false, false, true><<<grid, kThreads, Layout<D, false, true>::kAlloc, stream>>>(
+      tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return -1;
   if (may_cut) {
     combine_parts_kernel<D><<<2 * kCutUnits, kCombineThreads, 0, stream>>>(p.sched, p.part_o, p.part_lse, p.o, p.lse,
-                                                                           p.o_stride, p.T, p.H);
+                                                                           p.o_stride, p.T, p.pack);
     if (cudaGetLastError() != cudaSuccess) return -1;
   }
   return 0;
@@ -1553,10 +1752,10 @@ int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap
 
 }  // namespace
 
-// The schedule, then the parts' rows and log2-sum-exps (at most twice
-// kCutUnits parts of kRowsPerWork rows).
+// The schedule, then the parts' rows and log2-sum-exps (at most kCutUnits
+// parts of kRowsPerWork rows).
 size_t cross_attn_workspace_bytes(int B, int D) {
-  return cross_sched_bytes(B) + static_cast<size_t>(2 * kCutUnits) * kRowsPerWork * (D + 1) * sizeof(float);
+  return cross_sched_bytes(B) + static_cast<size_t>(kCutUnits) * kRowsPerWork * (D + 1) * sizeof(float);
 }
 
 int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* o, float* lse, int64_t q_stride,
@@ -1566,7 +1765,13 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
                              cudaStream_t stream, int num_sms) {
   CUtensorMap tq, tk, tv;
   // without any key there is nothing to map: the maps are never read then
-  if (!make_qkv_map(&tq, q, Tq, H, D, q_stride)) return -2;
+  const int group = H / Hkv;
+  // heads of one key head in one unit. Past 32 of them a query tile's 128 rows
+  // may be a quarter empty (128 mod pack), and K and V are read 32 times less
+  // often than the queries' rows as it is.
+  const int pack = group <= 32 ? group : 1;
+  const int tile_q = kBM / pack;
+  if (!make_qkv_map(&tq, q, Tq, H, D, q_stride, tile_q, pack)) return -2;
   if (Tk > 0 ? !make_qkv_map(&tk, k, Tk, Hkv, D, k_stride) || !make_qkv_map(&tv, v, Tk, Hkv, D, v_stride) : false)
     return -2;
   if (Tk == 0) tk = tv = tq;
@@ -1575,7 +1780,8 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   while (sort_n < B) sort_n <<= 1;
   const size_t sched_smem = B <= kSortLimit ? static_cast<size_t>(sort_n) * 8 : 0;
   if (sched_smem > 48 * 1024 && !set_schedule_smem_attr<true>()) return -1;
-  build_cross_schedule_kernel<<<1, kSchedThreads, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H, sched, status);
+  build_cross_schedule_kernel<<<1, kSchedThreads, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q,
+                                                                        sched, status);
   if (cudaGetLastError() != cudaSuccess) return -1;
   AttnParams p = {};
   p.o = static_cast<__nv_bfloat16*>(o);
@@ -1587,13 +1793,14 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   p.sched = sched;
   p.status = status;
   p.timeout_ns = timeout_ns;
-  p.group = H / Hkv;
+  p.pack = pack;
+  p.group = group;
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + cross_sched_bytes(B));
-  p.part_lse = p.part_o + static_cast<size_t>(2 * kCutUnits) * kRowsPerWork * D;
+  p.part_lse = p.part_o + static_cast<size_t>(kCutUnits) * kRowsPerWork * D;
   // no request has more than kMinPartTiles key tiles: no tile can be cut
   const bool may_cut = Tk > static_cast<int64_t>(kMinPartTiles) * kBN;
-  const int64_t max_units = static_cast<int64_t>(H) * ((Tq + kRowsPerWork - 1) / kRowsPerWork + B) +
-                            (may_cut ? kCutUnits : 0);
+  const int64_t tiles = static_cast<int64_t>(H / pack) * ((Tq + 2 * tile_q - 1) / (2 * tile_q) + B);
+  const int64_t max_units = tiles + (may_cut ? kCutUnits : 0);
   const int grid = static_cast<int>(max_units < num_sms ? max_units : num_sms);
   return D == 128 ? launch_cross<128>(tq, tk, tv, p, grid, may_cut, stream)
                   : launch_cross<64>(tq, tk, tv, p, grid, may_cut, stream);

@@ -41,7 +41,7 @@ def check(q, k, v, cu_q, cu_k, o, lse, scale=None):
         gl = lse.cpu().numpy().astype(np.float64)[:, :n]
         empty = np.isneginf(rl)
         assert np.array_equal(np.isneginf(gl), empty)
-        assert (np.abs(gl - rl)[~empty] <= 1e-5 * (1 + np.abs(rl[~empty]))).all()
+        assert (np.abs(gl[~empty] - rl[~empty]) <= 1e-5 * (1 + np.abs(rl[~empty]))).all()
 
 
 CASES = [
@@ -64,6 +64,39 @@ def test_every_element(lens_q, lens_k, H, Hkv, D):
         assert o.shape == (0, H, D)
         return
     o, lse = pqk.varlen_cross_attn_fwd(to_dev_bf16(q), to_dev_bf16(k), to_dev_bf16(v), to_dev(cu_q), to_dev(cu_k),
+                                       want_lse=True)
+    torch.cuda.synchronize()
+    assert pqk.get_device_status() == 0
+    check(q, k, v, cu_q, cu_k, o, lse)
+
+
+@pytest.mark.parametrize("H, Hkv, D", [(6, 2, 128), (10, 2, 64), (7, 1, 128), (27, 1, 64), (32, 1, 128), (40, 1, 64),
+                                       (16, 8, 128)])
+@pytest.mark.parametrize("lens_q, lens_k", [
+    ([1], [1]), ([1, 2, 3], [2000, 1500, 700]), ([43, 130, 4, 5], [130, 20, 600, 515]), ([300, 0, 9], [700, 4, 0]),
+    ([1, 4, 60, 200], [40000, 1, 513, 640])])
+def test_query_heads_that_share_key_heads(lens_q, lens_k, H, Hkv, D):
+    """Shared key heads put several query heads' rows in one tile: groups that do and do not divide 128, tiles and
+    keys that are cut or not, and (one key head for 40) the path that takes each head alone."""
+    torch = torch_cuda()
+    q, k, v, cu_q, cu_k = _inputs(lens_q, lens_k, H, Hkv, D, seed=H + sum(lens_q))
+    o = torch.full((sum(lens_q) + 3, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, sum(lens_q)), 7.0, device="cuda")
+    pqk.varlen_cross_attn_fwd(to_dev_bf16(q), to_dev_bf16(k), to_dev_bf16(v), to_dev(cu_q), to_dev(cu_k),
+                              o=o[:sum(lens_q)], lse=lse)
+    torch.cuda.synchronize()
+    assert pqk.get_device_status() == 0 and (o[sum(lens_q):] == 7.0).all()
+    check(q, k, v, cu_q, cu_k, o[:sum(lens_q)], lse)
+
+
+@pytest.mark.parametrize("n_q", [1, 128, 129, 256])
+@pytest.mark.parametrize("n_k", [512, 513, 640, 641, 768, 896, 1025, 1300])
+def test_keys_cut_into_parts(n_q, n_k):
+    """Parts of two, three and more key tiles, the last one ragged: the softmax groups take turns (up to 128
+    queries) or share each tile."""
+    torch = torch_cuda()
+    q, k, v, cu_q, cu_k = _inputs([n_q], [n_k], 2, 2, 128, seed=n_q + n_k)
+    o, lse = pqk.varlen_cross_attn_fwd(*(to_dev_bf16(t) for t in (q, k, v)), to_dev(cu_q), to_dev(cu_k),
                                        want_lse=True)
     torch.cuda.synchronize()
     assert pqk.get_device_status() == 0
