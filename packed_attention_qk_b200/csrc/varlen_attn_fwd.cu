@@ -159,19 +159,20 @@ struct Layout {
   static constexpr int kOutOff = kKVOff + kStages * kStageBytes;
   static constexpr int kBarOff = kOutOff + (kCross ? 8 * 32 * 128 : 0);
   // barriers: kv_full[S], kv_empty[S], q_full, q_empty, s_full[2], p_full[2], o_done[2], drain,
-  // work_full[kWorkSlots]
-  static constexpr int kNumBars = 2 * kStages + 9 + kWorkSlots;
+  // work_full[kWorkSlots], and for cross-attention q_full and q_empty of the second query tile
+  static constexpr int kNumBars = 2 * kStages + 9 + kWorkSlots + (kCross ? 2 : 0);
   static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
   static constexpr int kAbortOff = kTmemSlotOff + 4;
   // block-skip votes: one byte per softmax warp, [group][tile parity][warp]
   static constexpr int kVoteOff = kAbortOff + 4;
   // claimed work-tile indices, a ring of kWorkSlots (-1: no more work)
   static constexpr int kWorkOff = kVoteOff + 16;
-  // the producer's copy counts (K/V stages, Q pairs), left for the drain
+  // the producer's copy counts (K/V stages, Q pairs; kCross: K/V stages, first and second Q tiles), left for the
+  // drain
   // (kCross: the decoded units instead, eight words each)
   static constexpr int kUnitOff = (kWorkOff + 15) / 16 * 16;
   static constexpr int kLoadsOff = kCross ? kUnitOff + 32 * kWorkSlots : kWorkOff + 4 * kWorkSlots;
-  static constexpr int kBytes = kLoadsOff + 8;
+  static constexpr int kBytes = kLoadsOff + (kCross ? 12 : 8);
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024
   static constexpr uint32_t kTmemS0 = 0, kTmemS1 = 128, kTmemO0 = 256, kTmemO1 = 256 + D;
   static_assert(kAlloc <= 232448, "shared memory budget");
@@ -759,6 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_done = [&](int i) { return q_full + 48 + 8u * i; };
   const uint32_t drain = q_full + 64;
   auto work_full = [&](int i) { return q_full + 72 + 8u * i; };
+  // kCross: the two query tiles come and go separately
+  const uint32_t q1_full = q_full + 72 + 8u * kWorkSlots, q1_empty = q1_full + 8;
   volatile int* work_slot = reinterpret_cast<volatile int*>(smem + (kCross ? L::kUnitOff : L::kWorkOff));
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kTmemSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbortOff);
@@ -776,6 +779,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
+    if constexpr (kCross) {
+      mbar_init(q1_full, 1);
+      mbar_init(q1_empty, 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
       // one arrival per softmax thread, or on a pair one per softmax warp of either CTA
@@ -850,6 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp) {
     // ------------------------------------------------ TMA producer
     if (lane == 0) {
+      if (kCross) loads_done[2] = 0;
       uint32_t load_idx = 0;
       uint32_t q_loads = 0;
       bool ok = true;
@@ -918,9 +926,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           wk.head = -1;
           return w < n_work ? decode_cross(p.sched, p.pack, 2 * tile_q, w) : wk;
         };
+        auto load_q = [&](const CrossWork& wk, int i) {
+          mbar_arrive_expect_tx(i == 0 ? q_full : q1_full, q_tile_bytes);
+          for (int sl = 0; sl < L::kSlabs; ++sl)
+            tma_load_3d(q_smem + i * L::kTileBytes + sl * kSlabBytes, &tm_q, i == 0 ? q_full : q1_full, sl * 64,
+                        wk.head, wk.q0 + i * tile_q);
+        };
+        uint32_t q1_loads = 0;
         CrossWork wk = claim();
         for (int wt = 0;; ++wt) {
-          // the Q tiles of the previous unit are no longer needed: hand over the next one
+          // the first Q tile of the previous unit is no longer needed: hand over the next unit
           if (wt > 0 && !(ok = mbar_wait(q_empty, (wt - 1) & 1, abort_flag, p.timeout_ns))) break;
           volatile int* dst = work_slot + 8 * (wt % kWorkSlots);
           dst[0] = wk.head;
@@ -932,13 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           dst[6] = wk.slot;
           mbar_arrive(work_full(wt % kWorkSlots));
           if (wk.head < 0) break;
-          const int n_q = two_tiles(wk) ? 2 : 1;
-          mbar_arrive_expect_tx(q_full, n_q * q_tile_bytes);
+          load_q(wk, 0);
           ++q_loads;
-          for (int i = 0; i < n_q; ++i)
-            for (int sl = 0; sl < L::kSlabs; ++sl)
-              tma_load_3d(q_smem + i * L::kTileBytes + sl * kSlabBytes, &tm_q, q_full, sl * 64, wk.head,
-                          wk.q0 + i * tile_q);
           const int kv_head = wk.head / p.group;
           for (int i = 0; i < 2 * wk.n_kv; ++i) {  // K_0, V_0, K_1, V_1, ...
             const int s = load_idx % L::kStages;
@@ -950,9 +960,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, tm, kv_full(s), sl * 64, kv_head,
                           wk.k_start + (i >> 1) * kBN);
             ++load_idx;
+            if (i == 0 && two_tiles(wk)) {
+              // the second Q tile once the last unit that had one is through with it
+              if (q1_loads > 0 && !(ok = mbar_wait(q1_empty, (q1_loads - 1) & 1, abort_flag, p.timeout_ns))) break;
+              load_q(wk, 1);
+              ++q1_loads;
+            }
           }
+          loads_done[2] = q1_loads;
           if (!ok) break;
-          wk = claim();  // while the unit's last key tiles are worked on
+          // while the unit's last key tiles are worked on: the next unit, and its queries into L2
+          wk = claim();
+          if (wk.head >= 0)
+            for (int i = 0; i < (two_tiles(wk) ? 2 : 1); ++i)
+              for (int sl = 0; sl < L::kSlabs; ++sl) tma_prefetch_3d(&tm_q, sl * 64, wk.head, wk.q0 + i * tile_q);
         }
       } else {
       for (int wt = 0; ok; ++wt) {
@@ -1025,6 +1046,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto group_skips = [&](int i, int j) {
         return *reinterpret_cast<volatile uint32_t*>(votes + (i * 2 + (j & 1)) * 4) == 0x01010101u;
       };
+      // kCross: units with a second query tile so far (their second Q tiles' phase), and whether the unit's first
+      // S0 = Q0 K_0^T is already issued
+      uint32_t q1_phase = 0;
+      bool s0_issued = false;
       int wt = 0;
       bool ok = true;
       // Descriptor low words of Q0 and of stage 0 (K: K-major, V: MN-major
@@ -1145,18 +1170,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
         }
-        if (!(ok = mbar_wait(q_full, wt & 1, abort_flag, p.timeout_ns))) break;
         uint32_t k_stage_idx = cons_idx;
-        if (!(ok = wait_stage(k_stage_idx))) break;
-        tc_fence_after_sync();
-        issue_qk(0, k_stage_idx % L::kStages);
-        commit_all(s_full(0));
+        if (!s0_issued) {
+          if (!(ok = mbar_wait(q_full, wt & 1, abort_flag, p.timeout_ns))) break;
+          if (!(ok = wait_stage(k_stage_idx))) break;
+          tc_fence_after_sync();
+          issue_qk(0, k_stage_idx % L::kStages);
+          commit_all(s_full(0));
+          if (kCross && wk.n_kv == 1) commit_own(q_empty);
+        }
+        s0_issued = false;
         if (two) {
+          if constexpr (kCross) {
+            if (!(ok = mbar_wait(q1_full, q1_phase, abort_flag, p.timeout_ns))) break;
+            q1_phase ^= 1u;
+            tc_fence_after_sync();
+          }
           issue_qk(1, k_stage_idx % L::kStages);
           commit_all(s_full(1));
         }
         commit_own(kv_empty(k_stage_idx % L::kStages));
-        if (wk.n_kv == 1) commit_own(q_empty);
+        if (wk.n_kv == 1 && two) commit_own(kCross ? q1_empty : q_empty);
         ++cons_idx;
         // stages of iteration j: V_j and K_{j+1}
         uint32_t v_idx = cons_idx++;
@@ -1179,6 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) {
             issue_qk(0, nk_idx % L::kStages);
             commit_all(s_full(0));
+            if (kCross && j + 2 == wk.n_kv) commit_own(q_empty);
           }
           uint32_t next_v = 0, next_nk = 0;
           if (more) {
@@ -1197,12 +1232,41 @@ __global__ void __launch_bounds__(kThreads, 1)
               commit_own(kv_empty(v_idx % L::kStages));
               if (more) {
                 commit_own(kv_empty(nk_idx % L::kStages));
-                if (j + 2 == wk.n_kv) commit_own(q_empty);
               }
               p_phase ^= 1u;
               v_idx = next_v;
               nk_idx = next_nk;
               continue;
+            }
+          }
+          if constexpr (kCross) {
+            // After the unit's last O0 += P0 V: the next unit's first
+            // S0 = Q0 K_0^T as soon as its copies have landed, if that is
+            // before P1 is ready, so that the first softmax group need not
+            // wait for the second's. (Units without second query tile wait
+            // for the second group's arrival first, above.)
+            if (!more) {
+              const uint64_t t0 = global_timer_ns();
+              for (uint32_t polls = 1; !mbar_test_wait(p_full(1), p_phase1); ++polls) {
+                if (!s0_issued && mbar_test_wait(work_full((wt + 1) % kWorkSlots), ((wt + 1) / kWorkSlots) & 1) &&
+                    mbar_test_wait(q_full, (wt + 1) & 1) &&
+                    mbar_test_wait(kv_full(cons_idx % L::kStages), (cons_idx / L::kStages) & 1)) {
+                  const auto next = decode(wt + 1, 0);
+                  if (two_tiles(next)) {
+                    tc_fence_after_sync();
+                    issue_qk(0, cons_idx % L::kStages);
+                    commit_all(s_full(0));
+                    if (next.n_kv == 1) commit_own(q_empty);
+                    s0_issued = true;
+                  }
+                }
+                if (*abort_flag || polls >= kMaxPolls ||
+                    static_cast<long long>(global_timer_ns() - t0) > p.timeout_ns) {
+                  ok = false;
+                  break;
+                }
+              }
+              if (!ok) break;
             }
           }
           if (!(ok = mbar_wait(p_full(1), kCross ? p_phase1 : p_phase, abort_flag, p.timeout_ns))) break;
@@ -1218,7 +1282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_qk(1, nk_idx % L::kStages);
             commit_all(s_full(1));
             commit_own(kv_empty(nk_idx % L::kStages));
-            if (j + 2 == wk.n_kv) commit_own(q_empty);
+            if (j + 2 == wk.n_kv) commit_own(kCross ? q1_empty : q_empty);
           }
           p_phase ^= 1u;
           p_phase1 ^= 1u;
@@ -1501,7 +1565,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // at the cluster barrier meanwhile.
   if (*abort_flag) {
     if (leader && warp == kProducerWarp && lane == 0)
+    {
       drain_copies(kv_full(0), q_full, L::kStages, loads_done[0], loads_done[1]);
+      if (kCross && loads_done[2] > 0) mbar_drain_wait(q1_full, (loads_done[2] - 1) & 1);
+    }
     else if (leader && warp == kMmaWarp && lane == 0)
       kPair ? drain_mmas_pair(drain) : drain_mmas(drain);
     block_sync();
