@@ -201,6 +201,7 @@ struct AttnParams {
   const float* deq;                      // kFp8: [2H] dequantisation factors of Q's, then K's heads
   unsigned long long* skip_counts;       // nullable: [0] skipped warp blocks, [1] skipped O += P V products
   int pack;                              // kCross: query heads per unit
+  uint32_t pack_mul;                     // kCross: floor(2^16 / pack) + 1
   int group;                             // kCross: query heads per key head
   float* part_o;                         // kCross: [slots][kRowsPerWork][D] rows of cut tiles, and their
   float* part_lse;                       // [slots][kRowsPerWork] log2-sum-exps
@@ -360,17 +361,18 @@ constexpr int kSchedSmem = kSortLimit * 8;
 // (the request in each key's low word): a bitonic sort of the keys
 // (INT32_MAX - length) << 32 | index over the next power of two, padded with
 // keys above every real one. By the whole block.
+template <int kThreadsN>
 __device__ __forceinline__ void sort_longest_first(const int32_t* cu, int B, uint64_t* sort_keys) {
   int n = 1;
   while (n < B) n <<= 1;
-  for (int i = threadIdx.x; i < n; i += kSchedThreads)
+  for (int i = threadIdx.x; i < n; i += kThreadsN)
     sort_keys[i] = i < B ? (static_cast<uint64_t>(static_cast<uint32_t>(INT32_MAX - (cu[i + 1] - cu[i]))) << 32) |
                                static_cast<uint32_t>(i)
                          : ~0ull;
   __syncthreads();
   for (int k = 2; k <= n; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < n; i += kSchedThreads) {
+      for (int i = threadIdx.x; i < n; i += kThreadsN) {
         const int partner = i ^ j;
         if (partner > i) {
           const uint64_t a = sort_keys[i], b = sort_keys[partner];
@@ -386,13 +388,13 @@ __device__ __forceinline__ void sort_longest_first(const int32_t* cu, int B, uin
 }
 
 // out[i] = count(0) + ... + count(i - 1) for i < B; returns the total to every
-// thread. One chunk of kSchedThreads requests at a time (warp scans, then a
+// thread. One chunk of kThreadsN requests at a time (warp scans, then a
 // scan of warp sums). By the whole block.
-template <typename Count>
+template <int kThreadsN, typename Count>
 __device__ __forceinline__ int32_t exclusive_prefix(int B, int32_t* out, Count count) {
-  __shared__ int32_t warp_sums[kSchedThreads / 32];
+  __shared__ int32_t warp_sums[kThreadsN / 32];
   int32_t carry = 0;
-  for (int base = 0; base < B; base += kSchedThreads) {
+  for (int base = 0; base < B; base += kThreadsN) {
     const int i = base + threadIdx.x;
     const int32_t n = i < B ? count(i) : 0;
     int32_t incl = n;
@@ -405,7 +407,7 @@ __device__ __forceinline__ int32_t exclusive_prefix(int B, int32_t* out, Count c
     if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = incl;
     __syncthreads();
     int32_t before = carry, all = carry;
-    for (int w = 0; w < kSchedThreads / 32; ++w) {
+    for (int w = 0; w < kThreadsN / 32; ++w) {
       if (w < static_cast<int>(threadIdx.x >> 5)) before += warp_sums[w];
       all += warp_sums[w];
     }
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
     return;
   }
   if (B <= kSortLimit) {
-    sort_longest_first(cu, B, sort_keys);
+    sort_longest_first<kSchedThreads>(cu, B, sort_keys);
     for (int r = threadIdx.x; r < B; r += kSchedThreads) {
       const int i = static_cast<int>(sort_keys[r] & 0xffffffffu);
       seg_start[r] = cu[i];
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
     }
   }
   __syncthreads();
-  const int32_t total = exclusive_prefix(
+  const int32_t total = exclusive_prefix<kSchedThreads>(
       B, tile_start, [&](int i) { return ((seg_len[i] + rows_per_work - 1) / rows_per_work) * H; });
   if (threadIdx.x == 0) {
     tile_start[B] = total;
@@ -471,9 +473,13 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
 constexpr int kCutUnits = 148;
 constexpr int kMinPartTiles = 4;
 
-__global__ void __launch_bounds__(kSchedThreads)
+// kThreadsN: a warp for up to 32 requests, whose barriers cost next to nothing
+// (3 requests: 14 us with 1,024 threads), else kSchedThreads.
+template <int kThreadsN>
+__global__ void __launch_bounds__(kThreadsN)
     build_cross_schedule_kernel(const int32_t* cu_q, const int32_t* cu_k, int B, int64_t Tq, int64_t Tk,
                                 int head_blocks, int tile_tokens, int32_t* sched, int* status) {
+  launch_dependents();
   extern __shared__ uint64_t sort_keys[];
   __shared__ int bad;
   __shared__ unsigned long long key_tiles;  // of all tiles together
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(kSchedThreads)
     most_tiles = 0;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < B; i += kSchedThreads)
+  for (int i = threadIdx.x; i < B; i += kThreadsN)
     if (cu_q[i + 1] < cu_q[i] || cu_k[i + 1] < cu_k[i]) bad = 1;
   __syncthreads();
   if (bad) {
@@ -495,8 +501,8 @@ __global__ void __launch_bounds__(kSchedThreads)
   }
   const CrossSched cs(sched, B);
   const bool sorted = B <= kSortLimit;
-  if (sorted) sort_longest_first(cu_k, B, sort_keys);
-  for (int r = threadIdx.x; r < B; r += kSchedThreads) {
+  if (sorted) sort_longest_first<kThreadsN>(cu_k, B, sort_keys);
+  for (int r = threadIdx.x; r < B; r += kThreadsN) {
     const int i = sorted ? static_cast<int>(sort_keys[r] & 0xffffffffu) : r;
     cs.q_start[r] = cu_q[i];
     cs.q_len[r] = cu_q[i + 1] - cu_q[i];
@@ -506,13 +512,13 @@ __global__ void __launch_bounds__(kSchedThreads)
   __syncthreads();
   auto tiles_of = [&](int r) { return (cs.q_len[r] + tile_tokens - 1) / tile_tokens * head_blocks; };
   auto key_tiles_of = [&](int r) { return (cs.k_len[r] + kBN - 1) / kBN; };
-  const int32_t tiles = exclusive_prefix(B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
-  const int32_t empty = exclusive_prefix(B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
+  const int32_t tiles = exclusive_prefix<kThreadsN>(B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
+  const int32_t empty = exclusive_prefix<kThreadsN>(B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
   int part_tiles = 0;
   if (tiles < kCutUnits) {
     unsigned long long mine = 0;
     int most = 0;
-    for (int r = threadIdx.x; r < B; r += kSchedThreads) {
+    for (int r = threadIdx.x; r < B; r += kThreadsN) {
       const int kt = cs.q_len[r] > 0 ? key_tiles_of(r) : 0;
       mine += static_cast<unsigned long long>(tiles_of(r)) * kt;
       most = max(most, kt);
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(kSchedThreads)
       if (threadIdx.x == 0) count = 0;
       __syncthreads();
       int n = 0;
-      for (int r = threadIdx.x; r < B; r += kSchedThreads)
+      for (int r = threadIdx.x; r < B; r += kThreadsN)
         if (cs.k_len[r] > 0) n += tiles_of(r) * cross_parts(key_tiles_of(r), mid);
       if (n != 0) atomicAdd(&count, n);
       __syncthreads();
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(kSchedThreads)
     }
     part_tiles = hi;
   }
-  const int32_t units = exclusive_prefix(B, cs.unit_start, [&](int r) {
+  const int32_t units = exclusive_prefix<kThreadsN>(B, cs.unit_start, [&](int r) {
     return cs.k_len[r] > 0 ? tiles_of(r) * cross_parts(key_tiles_of(r), part_tiles) : 0;
   });
   if (threadIdx.x == 0) {
@@ -556,36 +562,38 @@ __global__ void __launch_bounds__(kSchedThreads)
 
 // The rows of cut tiles from their parts' rows o_i and log2-sum-exps u_i:
 // O = sum_i 2^(u_i - u) o_i / sum_i 2^(u_i - u) with u the largest u_i, and
-// lse = (u + log2 of that sum) ln 2. One warp a row, the parts in order.
+// lse = (u + log2 of that sum) ln 2. Block x takes tile x (cut tiles are fewer
+// than kCutUnits), its rows shared among the blocks of one x; one warp a row,
+// the parts in order.
 constexpr int kCombineThreads = 256;
+constexpr int kCombineBlocks = 8;  // per tile
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_parts_kernel(const int32_t* sched, const float* part_o, const float* part_lse, __nv_bfloat16* o,
                          float* lse, int64_t o_stride, int64_t Tq, int pack) {
   const int B = sched[1], tiles = sched[3], part_tiles = sched[5];
-  if (part_tiles == 0) return;
+  const int tile = blockIdx.x;
+  if (part_tiles == 0 || tile >= tiles) return;
   const CrossSched cs(sched, B);
+  const int r = find_last(cs.tile_start, B, tile);
+  const int parts = cross_parts((cs.k_len[r] + kBN - 1) / kBN, part_tiles);
+  if (parts == 1) return;
   const int tokens = kBM / pack;  // queries of one query tile
+  const int q_len = cs.q_len[r];
+  const int nqb = (q_len + 2 * tokens - 1) / (2 * tokens);
+  const int local = tile - cs.tile_start[r];
+  const int q_tile0 = (local % nqb) * 2 * tokens;
+  const int in_tile = min(2 * tokens, q_len - q_tile0);  // the tile's queries
+  // rows of one query tile only: both softmax groups left some, 128 rows apart
+  const bool one = in_tile <= tokens;
+  const int n = one ? 2 * parts : parts;
+  const int64_t step = one ? kBM : kRowsPerWork;
+  const int64_t slot_row = (cs.unit_start[r] + static_cast<int64_t>(local) * parts) * kRowsPerWork;
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kCombineThreads / 32);
-  // row-major over the tiles, so that tiles with few queries spread over the warps
-  for (int i = blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5); i < tiles * kRowsPerWork; i += warps) {
-    const int tile = i % tiles, row = i / tiles;
-    const int r = find_last(cs.tile_start, B, tile);
-    const int parts = cross_parts((cs.k_len[r] + kBN - 1) / kBN, part_tiles);
-    if (parts == 1) continue;
-    const int q_len = cs.q_len[r];
-    const int nqb = (q_len + 2 * tokens - 1) / (2 * tokens);
-    const int local = tile - cs.tile_start[r];
-    const int q_tile0 = (local % nqb) * 2 * tokens;
-    const int in_tile = row & (kBM - 1);
-    const int q_row = q_tile0 + (row >> 7) * tokens + in_tile / pack;
-    if (in_tile >= tokens * pack || q_row >= q_len) continue;
-    // rows of one query tile only: both softmax groups left some, 128 rows apart
-    const bool one = q_tile0 + tokens >= q_len;
-    const int n = one ? 2 * parts : parts;
-    const int64_t step = one ? kBM : kRowsPerWork;
-    const int64_t row0 = (cs.unit_start[r] + static_cast<int64_t>(local) * parts) * kRowsPerWork + row;
+  for (int i = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5); i < in_tile * pack;
+       i += kCombineBlocks * (kCombineThreads / 32)) {
+    const int token = i / pack;
+    const int64_t row0 = slot_row + (token < tokens ? i : kBM + i - tokens * pack);
     const float* u = part_lse + row0;
     const float* src = part_o + row0 * D + lane * (D / 32);
     float top = -INFINITY;
@@ -595,21 +603,26 @@ __global__ void __launch_bounds__(kCombineThreads)
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float weight = ex2_approx(u[k * step] - top);
-      sum += weight;
-      const float2* v = reinterpret_cast<const float2*>(src + k * step * D);
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      // one part's weight a lane, then the parts in order, eight rows in flight
+      const float mine = k0 + lane < n ? ex2_approx(u[(k0 + lane) * step] - top) : 0.f;
+      const int m = min(32, n - k0);
+#pragma unroll 8
+      for (int k = 0; k < m; ++k) {
+        const float weight = __shfl_sync(0xffffffffu, mine, k);
+        sum += weight;
+        const float2* v = reinterpret_cast<const float2*>(src + (k0 + k) * step * D);
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        const float2 x = v[e];
-        acc[2 * e] = fmaf(weight, x.x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(weight, x.y, acc[2 * e + 1]);
+        for (int e = 0; e < D / 64; ++e) {
+          const float2 x = v[e];
+          acc[2 * e] = fmaf(weight, x.x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(weight, x.y, acc[2 * e + 1]);
+        }
       }
     }
     const float inv = 1.0f / sum;
-    const int64_t t = cs.q_start[r] + q_row;
-    const int head = local / nqb * pack + in_tile % pack;
+    const int64_t t = cs.q_start[r] + q_tile0 + token;
+    const int head = local / nqb * pack + i - token * pack;
     uint32_t* dst = reinterpret_cast<uint32_t*>(o + t * o_stride + head * D + lane * (D / 32));
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
@@ -817,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kCross) wait_for_primary();  // the schedule
   const int n_work = p.sched[0];
   int* claim_counter = const_cast<int*>(p.sched + 2);
   // copies issued by the producer thread (K/V stages, Q tile pairs), kept in
@@ -850,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return decode_work(p.sched, p.H, w);
     }
   };
+  auto unit_word = [&](int wt, int i) -> int { return work_slot[8 * (wt % kWorkSlots) + i]; };
   // kCross: queries of one query tile; whether a unit has rows for the second
   const int tile_q = kCross ? kBM / p.pack : kBM;
   auto two_tiles = [&](const auto& wk) { return !kCross || wk.q0 + tile_q < end_of_queries(wk); };
@@ -945,20 +960,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           dst[4] = wk.k_len;
           dst[5] = wk.n_kv;
           dst[6] = wk.slot;
+          dst[7] = static_cast<int>(load_idx);  // index of the unit's first copy
           mbar_arrive(work_full(wt % kWorkSlots));
           if (wk.head < 0) break;
           load_q(wk, 0);
           ++q_loads;
           const int kv_head = wk.head / p.group;
-          for (int i = 0; i < 2 * wk.n_kv; ++i) {  // K_0, V_0, K_1, V_1, ...
+          // Copy i of the unit is key tile i / 2's K (even i) or V. In a unit whose
+          // groups take turns S runs two tiles ahead of P V, so the order there is
+          // K_0, K_1, V_0, K_2, V_1, ..., V_{n-2}, V_{n-1}: that of their use (one
+          // query x 55,296 keys x 40 heads: 264 us for K_0, V_0, K_1, ..., where
+          // K_{j+2} could not be asked for before V_{j+1} had a stage; 183 us so,
+          // 6.2 TB/s. Copying the tiles into L2 ahead as well is slower, 192).
+          const bool turns = wk.slot >= 0 && !two_tiles(wk);
+          auto key_tile_of = [&](int i, bool& is_v) {
+            if (!turns) {
+              is_v = (i & 1) != 0;
+              return i >> 1;
+            }
+            const int t = (i - 2) >> 1;
+            is_v = i >= 2 && ((i & 1) == 0 || t + 2 >= wk.n_kv);
+            return i < 2 ? i : ((i & 1) == 0 ? t : (is_v ? t + 1 : t + 2));
+          };
+          for (int i = 0; i < 2 * wk.n_kv; ++i) {
+            bool is_v;
+            const int t = key_tile_of(i, is_v);
             const int s = load_idx % L::kStages;
             const uint32_t round = load_idx / L::kStages;
             if (round > 0 && !(ok = mbar_wait(kv_empty(s), (round - 1) & 1, abort_flag, p.timeout_ns))) break;
             mbar_arrive_expect_tx(kv_full(s), L::kTileBytes);
-            const CUtensorMap* tm = (i & 1) == 0 ? &tm_k : &tm_v;
             for (int sl = 0; sl < L::kSlabs; ++sl)
-              tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, tm, kv_full(s), sl * 64, kv_head,
-                          wk.k_start + (i >> 1) * kBN);
+              tma_load_3d(kv_smem + s * L::kStageBytes + sl * kSlabBytes, is_v ? &tm_v : &tm_k, kv_full(s), sl * 64,
+                          kv_head, wk.k_start + t * kBN);
             ++load_idx;
             if (i == 0 && two_tiles(wk)) {
               // the second Q tile once the last unit that had one is through with it
@@ -1131,32 +1164,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_phase1 ^= 1u;
           }
           // A part of a tile without second query tile: the groups take turns,
-          // group j % 2 on key tile j (there are at least two). The copies
-          // wanted at once, V_j to K_{j+2}, are at most four.
+          // group j % 2 on key tile j (there are at least two). Copies come in
+          // the order of their use, so a product waits for none but its own.
           if (!two && wk.slot >= 0) {
             if (!(ok = mbar_wait(q_full, wt & 1, abort_flag, p.timeout_ns))) break;
-            auto k_idx = [&](int j) { return cons_idx + 2 * j; };
             for (int j = 0; j < 2 && ok; ++j) {
-              if (!(ok = wait_stage(k_idx(j)))) break;
+              const uint32_t k_idx = cons_idx + j;
+              if (!(ok = wait_stage(k_idx))) break;
               tc_fence_after_sync();
-              issue_qk_of(j, 0, k_idx(j) % L::kStages);
+              issue_qk_of(j, 0, k_idx % L::kStages);
               commit_all(s_full(j));
-              commit_own(kv_empty(k_idx(j) % L::kStages));
+              commit_own(kv_empty(k_idx % L::kStages));
             }
             if (!ok) break;
             if (wk.n_kv == 2) commit_own(q_empty);
             for (int j = 0; j < wk.n_kv; ++j) {
               const int g = j & 1;
               const bool more = j + 2 < wk.n_kv;
-              const uint32_t v_idx = k_idx(j) + 1, nk_idx = k_idx(j + 2);
+              const uint32_t v_idx = cons_idx + (j + 1 < wk.n_kv ? 2 * j + 2 : 2 * j + 1);
               if (!(ok = wait_stage(v_idx))) break;
-              if (more && !(ok = wait_stage(nk_idx))) break;
               if (!(ok = mbar_wait(p_full(g), g == 0 ? p_phase : p_phase1, abort_flag, p.timeout_ns))) break;
               if (g == 0) p_phase ^= 1u; else p_phase1 ^= 1u;
               tc_fence_after_sync();
               issue_pv(g, v_idx % L::kStages, j >= 2);
               commit_own(kv_empty(v_idx % L::kStages));
               if (more) {
+                const uint32_t nk_idx = cons_idx + 2 * j + 3;
+                if (!(ok = wait_stage(nk_idx))) break;
+                tc_fence_after_sync();
                 issue_qk_of(g, 0, nk_idx % L::kStages);
                 commit_all(s_full(g));
                 commit_own(kv_empty(nk_idx % L::kStages));
@@ -1297,12 +1332,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ softmax groups
     const int grp = warp >> 2;  // 0 -> Q0, 1 -> Q1
     const int r = threadIdx.x & 127;
+    // kCross: a query tile's row -> its token, r / pack (exact for r < 128, pack <= 32: the factor is
+    // floor(2^16 / pack) + 1)
+    auto token_of = [&](int row_in_tile) { return static_cast<int>((row_in_tile * p.pack_mul) >> 16); };
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + (grp == 0 ? L::kTmemS0 : L::kTmemS1);
     const uint32_t t_o = tmem + lane_off + (grp == 0 ? L::kTmemO0 : L::kTmemO1);
     uint32_t s_phase = 0;
-    uint32_t o_phase = 0;      // kCross: this group's count of units, as a parity
-    uint32_t kv_idx = 0;       // kCross: index of the unit's first K copy
+    uint32_t o_phase = 0;  // kCross: this group's count of units, as a parity
     int wt = 0;
     bool ok = true;
     unsigned long long warp_skips = 0;
@@ -1317,24 +1354,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         turns = wk.slot >= 0 && !two_tiles(wk);
         if (grp == 1 && !turns && !two_tiles(wk)) {
           mbar_arrive(p_full(1));
-          kv_idx += 2 * wk.n_kv;
           continue;
         }
       }
-      const int first_j = turns ? grp : 0, step_j = turns ? 2 : 1;
-      const int last_keys = key_count(wk) - (wk.n_kv - 1) * kBN;  // in the last key tile
+      const int step_j = turns ? 2 : 1;
+      const int n_kv = wk.n_kv;
       const int row = kCross ? 0 : wk.q0 + static_cast<int>(rank) * kRowsPerWork + grp * kBM + r;
       // log2-domain score factor; FP8 scores carry the two heads' dequantisation factors
       const float sl2 = kFp8 ? p.scale_log2 * p.deq[wk.head] * p.deq[p.H + wk.head] : p.scale_log2;
       float m = -INFINITY, l = 0.f;
       float m_seen = -INFINITY;  // block skipping: running maximum over all earlier tiles
-      for (int j = first_j; j < wk.n_kv; j += step_j) {
+      for (int j = turns ? grp : 0; j < n_kv; j += step_j) {
         ok = __all_sync(0xffffffffu, mbar_wait(s_full(grp), s_phase, abort_flag, p.timeout_ns));
         if (!ok) break;
         s_phase ^= 1u;
         tc_fence_after_sync();
         // keys at or past the request end (last tile only) are masked
-        const int valid = j == wk.n_kv - 1 ? (kCross ? last_keys : key_count(wk) - j * kBN) : kBN;
+        // (kCross: what the loop seldom needs is read from the unit's slot again, not held in a register)
+        const int valid = j == n_kv - 1 ? (kCross ? unit_word(wt, 4) : key_count(wk)) - j * kBN : kBN;
         float s[128];
         load_scores(t_s, valid, s);
         const float mx = row_max(s) * sl2;
@@ -1399,7 +1436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // them (the first group's "P ready" precedes both groups' products;
           // when they take turns, the tile is this group's alone)
           if ((grp == 0 || turns) && valid < kBN) {
-            const uint32_t idx = kv_idx + 2 * j + 1;
+            const uint32_t idx = static_cast<uint32_t>(unit_word(wt, 7)) + 2 * j + 1;  // the unit's last copy
             const int st = idx % L::kStages;
             ok = __all_sync(0xffffffffu, mbar_wait(kv_full(st), (idx / L::kStages) & 1, abort_flag, p.timeout_ns));
             if (!ok) break;
@@ -1433,7 +1470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(o_done(grp), kCross ? o_phase : wt & 1, abort_flag, p.timeout_ns));
       if (!ok) break;
       o_phase ^= 1u;
-      kv_idx += 2 * wk.n_kv;
       tc_fence_after_sync();
       // FP8 P V accumulates V's codes: its dequantisation factor comes in here
       const float inv_l = (kFp8Pv ? p.deq[2 * p.H + wk.head] : 1.0f) / l;
@@ -1443,7 +1479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // over the key tiles cost spills
         const auto un = decode(wt, w);
         // this thread's token and head, of the query tile's tile_q x pack rows
-        const int r_token = r / p.pack;
+        const int r_token = token_of(r);
         const int q_row = un.q0 + (un.slot >= 0 && !two_tiles(un) ? 0 : grp * tile_q) + r_token;
         const bool valid_row = r_token < tile_q && q_row < un.q_end;
         if (un.slot >= 0) {
@@ -1531,7 +1567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = find_last(cs.empty_start, B, i);
         const int nqb = (cs.q_len[q] + 2 * tile_q - 1) / (2 * tile_q);
         const int local = i - cs.empty_start[q];
-        const int r_token = r / p.pack;
+        const int r_token = token_of(r);
         const int head = local / nqb * p.pack + r - r_token * p.pack;
         const int in_request = (local % nqb) * 2 * tile_q + grp * tile_q + r_token;
         if (r_token < tile_q && in_request < cs.q_len[q]) {
@@ -1652,7 +1688,7 @@ bool set_schedule_smem_attr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(kCross ? reinterpret_cast<const void*>(build_cross_schedule_kernel)
+    if (cudaFuncSetAttribute(kCross ? reinterpret_cast<const void*>(build_cross_schedule_kernel<kSchedThreads>)
                                     : reinterpret_cast<const void*>(build_schedule_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedSmem) !=
         cudaSuccess)
       return false;
@@ -1806,12 +1842,24 @@ template <int D>
 int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, int grid,
                  bool may_cut, cudaStream_t stream) {
   if (!set_smem_attr<D, false, false, false, true>()) return -1;
-  attn_fwd_kernel<D, false, false, false, false, true><<<grid, kThreads, Layout<D, false, true>::kAlloc, stream>>>(
-      tq, tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  // The attention kernel sets itself up while the schedule is still being
+  // built (programmatic dependent launch) and waits for it where it first
+  // needs it.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Layout<D, false, true>::kAlloc;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, false, false, false, false, true>, tq, tk, tv, p) != cudaSuccess)
+    return -1;
   if (may_cut) {
-    combine_parts_kernel<D><<<2 * kCutUnits, kCombineThreads, 0, stream>>>(p.sched, p.part_o, p.part_lse, p.o, p.lse,
-                                                                           p.o_stride, p.T, p.pack);
+    combine_parts_kernel<D><<<dim3(kCutUnits, kCombineBlocks), kCombineThreads, 0, stream>>>(
+        p.sched, p.part_o, p.part_lse, p.o, p.lse, p.o_stride, p.T, p.pack);
     if (cudaGetLastError() != cudaSuccess) return -1;
   }
   return 0;
@@ -1847,7 +1895,11 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   while (sort_n < B) sort_n <<= 1;
   const size_t sched_smem = B <= kSortLimit ? static_cast<size_t>(sort_n) * 8 : 0;
   if (sched_smem > 48 * 1024 && !set_schedule_smem_attr<true>()) return -1;
-  build_cross_schedule_kernel<<<1, kSchedThreads, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q,
+  if (B <= 32)
+    build_cross_schedule_kernel<32><<<1, 32, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q,
+                                                                        sched, status);
+  else
+    build_cross_schedule_kernel<kSchedThreads><<<1, kSchedThreads, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q,
                                                                         sched, status);
   if (cudaGetLastError() != cudaSuccess) return -1;
   AttnParams p = {};
@@ -1861,6 +1913,7 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   p.status = status;
   p.timeout_ns = timeout_ns;
   p.pack = pack;
+  p.pack_mul = 65536 / pack + 1;
   p.group = group;
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + cross_sched_bytes(B));
   p.part_lse = p.part_o + static_cast<size_t>(kCutUnits) * kRowsPerWork * D;

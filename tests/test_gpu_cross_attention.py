@@ -159,6 +159,13 @@ def test_strides_scale_and_peaked_rows():
     assert pqk.get_device_status() == 0
     check(q, k, v, cu_q, cu_k, o, lse, scale=0.25)
     assert (ow[:, :2] == 9.0).all()
+    # rows of the output on 16-byte but not on 32-byte boundaries
+    flat = torch.full((q.shape[0] * (H * D + 8) + 8,), 9.0, dtype=torch.bfloat16, device="cuda")
+    odd = flat[8:].view(q.shape[0], H * D + 8)[:, :H * D].unflatten(1, (H, D))
+    assert odd.data_ptr() % 32 == 16
+    o2, _ = pqk.varlen_cross_attn_fwd(qw[:, 1:1 + H], kv[:, :Hkv], kv[:, Hkv:2 * Hkv], to_dev(cu_q), to_dev(cu_k),
+                                      softmax_scale=0.25, o=odd)
+    assert torch.equal(o2, o) and (flat[:8] == 9.0).all() and (flat[8:].view(-1, H * D + 8)[:, H * D:] == 9.0).all()
 
 
 def test_equal_lengths_are_self_attention():
