@@ -473,10 +473,7 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
 constexpr int kCutUnits = 148;
 constexpr int kMinPartTiles = 4;
 
-// kThreadsN: a warp for up to 32 requests, whose barriers cost next to nothing
-// (3 requests: 14 us with 1,024 threads), else kSchedThreads.
-template <int kThreadsN>
-__global__ void __launch_bounds__(kThreadsN)
+__global__ void __launch_bounds__(kSchedThreads)
     build_cross_schedule_kernel(const int32_t* cu_q, const int32_t* cu_k, int B, int64_t Tq, int64_t Tk,
                                 int head_blocks, int tile_tokens, int32_t* sched, int* status) {
   launch_dependents();
@@ -491,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsN)
     most_tiles = 0;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < B; i += kThreadsN)
+  for (int i = threadIdx.x; i < B; i += kSchedThreads)
     if (cu_q[i + 1] < cu_q[i] || cu_k[i + 1] < cu_k[i]) bad = 1;
   __syncthreads();
   if (bad) {
@@ -501,8 +498,8 @@ __global__ void __launch_bounds__(kThreadsN)
   }
   const CrossSched cs(sched, B);
   const bool sorted = B <= kSortLimit;
-  if (sorted) sort_longest_first<kThreadsN>(cu_k, B, sort_keys);
-  for (int r = threadIdx.x; r < B; r += kThreadsN) {
+  if (sorted) sort_longest_first<kSchedThreads>(cu_k, B, sort_keys);
+  for (int r = threadIdx.x; r < B; r += kSchedThreads) {
     const int i = sorted ? static_cast<int>(sort_keys[r] & 0xffffffffu) : r;
     cs.q_start[r] = cu_q[i];
     cs.q_len[r] = cu_q[i + 1] - cu_q[i];
@@ -512,13 +509,13 @@ __global__ void __launch_bounds__(kThreadsN)
   __syncthreads();
   auto tiles_of = [&](int r) { return (cs.q_len[r] + tile_tokens - 1) / tile_tokens * head_blocks; };
   auto key_tiles_of = [&](int r) { return (cs.k_len[r] + kBN - 1) / kBN; };
-  const int32_t tiles = exclusive_prefix<kThreadsN>(B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
-  const int32_t empty = exclusive_prefix<kThreadsN>(B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
+  const int32_t tiles = exclusive_prefix<kSchedThreads>(B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
+  const int32_t empty = exclusive_prefix<kSchedThreads>(B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
   int part_tiles = 0;
   if (tiles < kCutUnits) {
     unsigned long long mine = 0;
     int most = 0;
-    for (int r = threadIdx.x; r < B; r += kThreadsN) {
+    for (int r = threadIdx.x; r < B; r += kSchedThreads) {
       const int kt = cs.q_len[r] > 0 ? key_tiles_of(r) : 0;
       mine += static_cast<unsigned long long>(tiles_of(r)) * kt;
       most = max(most, kt);
@@ -535,7 +532,7 @@ __global__ void __launch_bounds__(kThreadsN)
       if (threadIdx.x == 0) count = 0;
       __syncthreads();
       int n = 0;
-      for (int r = threadIdx.x; r < B; r += kThreadsN)
+      for (int r = threadIdx.x; r < B; r += kSchedThreads)
         if (cs.k_len[r] > 0) n += tiles_of(r) * cross_parts(key_tiles_of(r), mid);
       if (n != 0) atomicAdd(&count, n);
       __syncthreads();
@@ -543,7 +540,7 @@ __global__ void __launch_bounds__(kThreadsN)
     }
     part_tiles = hi;
   }
-  const int32_t units = exclusive_prefix<kThreadsN>(B, cs.unit_start, [&](int r) {
+  const int32_t units = exclusive_prefix<kSchedThreads>(B, cs.unit_start, [&](int r) {
     return cs.k_len[r] > 0 ? tiles_of(r) * cross_parts(key_tiles_of(r), part_tiles) : 0;
   });
   if (threadIdx.x == 0) {
@@ -560,13 +557,93 @@ __global__ void __launch_bounds__(kThreadsN)
   }
 }
 
+// The same for at most 32 requests by one warp, a request a lane, without
+// barriers or a way through memory (3 requests: 3 us where the block above
+// takes 14).
+constexpr int kWarpRequests = 32;
+__global__ void __launch_bounds__(32)
+    build_cross_schedule_warp_kernel(const int32_t* cu_q, const int32_t* cu_k, int B, int64_t Tq, int64_t Tk,
+                                     int head_blocks, int tile_tokens, int32_t* sched, int* status) {
+  launch_dependents();
+  constexpr unsigned kAll = 0xffffffffu;
+  __shared__ int4 sorted[kWarpRequests];
+  const int lane = threadIdx.x;
+  const int at = min(lane, B);
+  const int q0 = cu_q[at], k0 = cu_k[at], q1 = cu_q[min(lane + 1, B)], k1 = cu_k[min(lane + 1, B)];
+  const bool bad = q1 < q0 || k1 < k0 || (lane == 0 && (q0 != 0 || k0 != 0)) ||
+                   static_cast<int64_t>(q1) > Tq || static_cast<int64_t>(k1) > Tk;
+  if (__any_sync(kAll, bad)) {
+    if (lane < kCrossHeader) sched[lane] = lane == 1 ? B : 0;
+    if (lane == 0) atomicCAS(status, 0, kStatusBadSeqlens);
+    return;
+  }
+  // longest keys first, ties by index; lanes past B hold requests of nothing
+  int rank = 0;
+  for (int i = 0; i < kWarpRequests; ++i) {
+    const int other = __shfl_sync(kAll, k1 - k0, i);
+    rank += other > k1 - k0 || (other == k1 - k0 && i < lane);
+  }
+  sorted[rank] = make_int4(q0, q1 - q0, k0, k1 - k0);
+  __syncwarp();
+  const int4 mine = sorted[lane];
+  const int all_tiles = (mine.y + tile_tokens - 1) / tile_tokens * head_blocks;
+  const int my_tiles = mine.w > 0 ? all_tiles : 0;
+  const int key_tiles = (mine.w + kBN - 1) / kBN;
+  // inclusive prefix over the lanes
+  auto scan = [&](int v) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(kAll, v, off);
+      if (lane >= off) v += y;
+    }
+    return v;
+  };
+  const int tiles_incl = scan(my_tiles), empty_incl = scan(all_tiles - my_tiles);
+  const int tiles = __shfl_sync(kAll, tiles_incl, 31), empty = __shfl_sync(kAll, empty_incl, 31);
+  int part_tiles = 0;
+  if (tiles < kCutUnits) {
+    unsigned long long total = static_cast<unsigned long long>(my_tiles) * key_tiles;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) total += __shfl_xor_sync(kAll, total, off);
+    int hi = max(__reduce_max_sync(kAll, my_tiles > 0 ? key_tiles : 0), kMinPartTiles);
+    int lo = max(kMinPartTiles, static_cast<int>((total + kCutUnits - 1) / kCutUnits));
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__reduce_add_sync(kAll, my_tiles * cross_parts(key_tiles, mid)) <= kCutUnits) hi = mid; else lo = mid + 1;
+    }
+    part_tiles = hi;
+  }
+  const int my_units = my_tiles * cross_parts(key_tiles, part_tiles);
+  const int units_incl = scan(my_units);
+  const CrossSched cs(sched, B);
+  if (lane < B) {
+    cs.unit_start[lane] = units_incl - my_units;
+    cs.tile_start[lane] = tiles_incl - my_tiles;
+    cs.empty_start[lane] = empty_incl - (all_tiles - my_tiles);
+    cs.q_start[lane] = mine.x;
+    cs.q_len[lane] = mine.y;
+    cs.k_start[lane] = mine.z;
+    cs.k_len[lane] = mine.w;
+  }
+  if (lane == 31) {
+    cs.unit_start[B] = units_incl;
+    cs.tile_start[B] = tiles;
+    cs.empty_start[B] = empty;
+    sched[0] = units_incl;
+    sched[1] = B;
+    sched[2] = 0;  // claim counter
+    sched[3] = tiles;
+    sched[4] = empty;
+    sched[5] = part_tiles;
+    sched[6] = sched[7] = 0;
+  }
+}
+
 // The rows of cut tiles from their parts' rows o_i and log2-sum-exps u_i:
 // O = sum_i 2^(u_i - u) o_i / sum_i 2^(u_i - u) with u the largest u_i, and
-// lse = (u + log2 of that sum) ln 2. Block x takes tile x (cut tiles are fewer
-// than kCutUnits), its rows shared among the blocks of one x; one warp a row,
-// the parts in order.
+// lse = (u + log2 of that sum) ln 2. Block (x, y) takes tile x's rows from 8 y
+// on, a warp a row, the parts in order.
 constexpr int kCombineThreads = 256;
-constexpr int kCombineBlocks = 8;  // per tile
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_parts_kernel(const int32_t* sched, const float* part_o, const float* part_lse, __nv_bfloat16* o,
@@ -590,8 +667,8 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int64_t step = one ? kBM : kRowsPerWork;
   const int64_t slot_row = (cs.unit_start[r] + static_cast<int64_t>(local) * parts) * kRowsPerWork;
   const int lane = threadIdx.x & 31;
-  for (int i = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5); i < in_tile * pack;
-       i += kCombineBlocks * (kCombineThreads / 32)) {
+  const int i = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5);
+  if (i < in_tile * pack) {
     const int token = i / pack;
     const int64_t row0 = slot_row + (token < tokens ? i : kBM + i - tokens * pack);
     const float* u = part_lse + row0;
@@ -604,10 +681,10 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
     for (int k0 = 0; k0 < n; k0 += 32) {
-      // one part's weight a lane, then the parts in order, eight rows in flight
+      // one part's weight a lane, then the parts in order, 16 rows in flight
       const float mine = k0 + lane < n ? ex2_approx(u[(k0 + lane) * step] - top) : 0.f;
       const int m = min(32, n - k0);
-#pragma unroll 8
+#pragma unroll 16
       for (int k = 0; k < m; ++k) {
         const float weight = __shfl_sync(0xffffffffu, mine, k);
         sum += weight;
@@ -1688,7 +1765,7 @@ bool set_schedule_smem_attr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(kCross ? reinterpret_cast<const void*>(build_cross_schedule_kernel<kSchedThreads>)
+    if (cudaFuncSetAttribute(kCross ? reinterpret_cast<const void*>(build_cross_schedule_kernel)
                                     : reinterpret_cast<const void*>(build_schedule_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedSmem) !=
         cudaSuccess)
       return false;
@@ -1839,8 +1916,8 @@ namespace {
 size_t cross_sched_bytes(int B) { return (cross_sched_words(B) * sizeof(int32_t) + 255) & ~static_cast<size_t>(255); }
 
 template <int D>
-int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, int grid,
-                 bool may_cut, cudaStream_t stream) {
+int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, int B,
+                 int grid, bool may_cut, cudaStream_t stream) {
   if (!set_smem_attr<D, false, false, false, true>()) return -1;
   // The attention kernel sets itself up while the schedule is still being
   // built (programmatic dependent launch) and waits for it where it first
@@ -1858,7 +1935,13 @@ int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap
   if (cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, false, false, false, false, true>, tq, tk, tv, p) != cudaSuccess)
     return -1;
   if (may_cut) {
-    combine_parts_kernel<D><<<dim3(kCutUnits, kCombineBlocks), kCombineThreads, 0, stream>>>(
+    // as many blocks as there can be cut tiles (fewer than kCutUnits) and rows in one
+    const int tokens = kBM / p.pack;
+    const int64_t tiles = static_cast<int64_t>(p.H / p.pack) * ((p.T + 2 * tokens - 1) / (2 * tokens) + B);
+    const int64_t rows = (p.T < 2 * tokens ? p.T : 2 * tokens) * p.pack;
+    const dim3 blocks(static_cast<unsigned>(tiles < kCutUnits ? tiles : kCutUnits),
+                      static_cast<unsigned>((rows + kCombineThreads / 32 - 1) / (kCombineThreads / 32)));
+    combine_parts_kernel<D><<<blocks, kCombineThreads, 0, stream>>>(
         p.sched, p.part_o, p.part_lse, p.o, p.lse, p.o_stride, p.T, p.pack);
     if (cudaGetLastError() != cudaSuccess) return -1;
   }
@@ -1895,12 +1978,11 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   while (sort_n < B) sort_n <<= 1;
   const size_t sched_smem = B <= kSortLimit ? static_cast<size_t>(sort_n) * 8 : 0;
   if (sched_smem > 48 * 1024 && !set_schedule_smem_attr<true>()) return -1;
-  if (B <= 32)
-    build_cross_schedule_kernel<32><<<1, 32, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q,
-                                                                        sched, status);
+  if (B <= kWarpRequests)
+    build_cross_schedule_warp_kernel<<<1, 32, 0, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q, sched, status);
   else
-    build_cross_schedule_kernel<kSchedThreads><<<1, kSchedThreads, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q,
-                                                                        sched, status);
+    build_cross_schedule_kernel<<<1, kSchedThreads, sched_smem, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q,
+                                                                          sched, status);
   if (cudaGetLastError() != cudaSuccess) return -1;
   AttnParams p = {};
   p.o = static_cast<__nv_bfloat16*>(o);
@@ -1922,8 +2004,8 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   const int64_t tiles = static_cast<int64_t>(H / pack) * ((Tq + 2 * tile_q - 1) / (2 * tile_q) + B);
   const int64_t max_units = tiles + (may_cut ? kCutUnits : 0);
   const int grid = static_cast<int>(max_units < num_sms ? max_units : num_sms);
-  return D == 128 ? launch_cross<128>(tq, tk, tv, p, grid, may_cut, stream)
-                  : launch_cross<64>(tq, tk, tv, p, grid, may_cut, stream);
+  return D == 128 ? launch_cross<128>(tq, tk, tv, p, B, grid, may_cut, stream)
+                  : launch_cross<64>(tq, tk, tv, p, B, grid, may_cut, stream);
 }
 
 int launch_wait_selftest(int* status, long long timeout_ns, cudaStream_t stream) {
