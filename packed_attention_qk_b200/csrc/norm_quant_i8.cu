@@ -24,14 +24,13 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "pqk_internal.h"
 
 namespace pqk {
 namespace {
-
-constexpr int kThreads = 256;
 
 struct NormQuantParams {
   const __nv_bfloat16* x;
@@ -114,9 +113,20 @@ struct MaxOp {
   __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
 
-template <int kTpr, int kCpt>
-__global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuantParams p) {
-  constexpr int kRows = kThreads / kTpr;
+// Threads per block, and the blocks per SM that the registers have to allow:
+// with 7 chunks a thread three blocks (80 registers) instead of two take a
+// [12,345, 13,824] quantisation from 127 to 104 us; elsewhere the compiler's
+// own choice is within 3 % of the best.
+template <int kTpr>
+constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
+template <int kTpr, int kCpt, bool kPlain>
+constexpr int kBlocksPerSm = kPlain && kTpr == 256 && kCpt >= 6 ? 3 : 1;
+
+// kPlain: codes of x alone (no branch, norm or vectors), in fewer registers.
+template <int kTpr, int kCpt, bool kPlain>
+__global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>)
+    norm_quant_i8_kernel(const NormQuantParams p) {
+  constexpr int kRows = kBlock<kTpr> / kTpr;
   // one set of words for each of a row's exchanges, so that no exchange can
   // overwrite words that a slow warp still reads
   __shared__ float s_sum[kRows][2][kTpr / 32];
@@ -126,7 +136,8 @@ __global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuant
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + group;
   if (t >= p.T) return;  // a whole row's threads leave together: barriers count one row's threads
   const int nchunks = p.C >> 3;
-  const int64_t mod_row = p.cu != nullptr ? static_cast<int64_t>(find_segment(p.cu, p.B, t)) * p.C : 0;
+  const int64_t mod_row =
+      !kPlain && p.cu != nullptr ? static_cast<int64_t>(find_segment(p.cu, p.B, t)) * p.C : 0;
 
   float v[kCpt][8];
   {
@@ -136,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuant
       const int c = lane + i * kTpr;
       xr[i] = c < nchunks ? ld_stream16(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
     }
-    if (p.branch != nullptr) {
+    if (!kPlain && p.branch != nullptr) {
 #pragma unroll
       for (int i = 0; i < kCpt; ++i) {
         const int c = lane + i * kTpr;
@@ -147,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuant
     for (int i = 0; i < kCpt; ++i) {
       const int c = lane + i * kTpr;
       unpack8(xr[i], v[i]);
-      if (p.branch != nullptr && c < nchunks) {
+      if (!kPlain && p.branch != nullptr && c < nchunks) {
         float b[8], g[8];
         unpack8(br[i], b);
         if (p.gate_res != nullptr) {
@@ -163,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuant
   }
   // x' of every element is formed by the thread that read the element: x_out
   // may be x (or branch) itself
-  if (p.x_out != nullptr) {
+  if (!kPlain && p.x_out != nullptr) {
 #pragma unroll
     for (int i = 0; i < kCpt; ++i) {
       const int c = lane + i * kTpr;
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuant
   }
 
   const float inv_c = 1.0f / static_cast<float>(p.C);
-  if (p.norm_type != 2) {
+  if (!kPlain && p.norm_type != 2) {
     float mu = 0.f;
     if (p.norm_type == 1) {
       float s = 0.f;
@@ -214,13 +225,13 @@ __global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuant
   for (int i = 0; i < kCpt; ++i) {
     const int c = lane + i * kTpr;
     if (c < nchunks) {
-      if (p.weight != nullptr) {
+      if (!kPlain && p.weight != nullptr) {
         float w[8];
         unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight + c * 8)), w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
       }
-      if (p.shift != nullptr) {
+      if (!kPlain && p.shift != nullptr) {
         float sc[8], sh[8];
         load8f(p.scale + mod_row + c * 8, sc);
         load8f(p.shift + mod_row + c * 8, sh);
@@ -258,10 +269,13 @@ __global__ void __launch_bounds__(kThreads) norm_quant_i8_kernel(const NormQuant
 }
 
 template <int kTpr, int kCpt>
-int launch(const NormQuantParams& p, cudaStream_t stream) {
-  constexpr int kRows = kThreads / kTpr;
-  const int64_t blocks = (p.T + kRows - 1) / kRows;
-  norm_quant_i8_kernel<kTpr, kCpt><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+int launch(const NormQuantParams& p, bool plain, cudaStream_t stream) {
+  constexpr int kRows = kBlock<kTpr> / kTpr;
+  const unsigned blocks = static_cast<unsigned>((p.T + kRows - 1) / kRows);
+  if (plain)
+    norm_quant_i8_kernel<kTpr, kCpt, true><<<blocks, kBlock<kTpr>, 0, stream>>>(p);
+  else
+    norm_quant_i8_kernel<kTpr, kCpt, false><<<blocks, kBlock<kTpr>, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
@@ -270,7 +284,7 @@ int launch(const NormQuantParams& p, cudaStream_t stream) {
 int launch_norm_quant_i8(const void* x, int64_t x_stride, const void* branch, int64_t branch_stride, void* x_out,
                          int64_t x_out_stride, void* h8, int64_t h8_stride, float* h_scale, const void* weight,
                          const float* shift, const float* scale, const float* gate_res, const int32_t* cu, int B,
-                         int64_t T, int C, int norm_type, float eps, cudaStream_t stream) {
+                         int64_t T, int C, int norm_type, float eps, cudaStream_t stream, int num_sms) {
   NormQuantParams p;
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.branch = static_cast<const __nv_bfloat16*>(branch);
@@ -291,11 +305,52 @@ int launch_norm_quant_i8(const void* x, int64_t x_stride, const void* branch, in
   p.C = C;
   p.norm_type = norm_type;
   p.eps = eps;
-  const int nchunks = C / 8;
-  if (nchunks <= 32 * 2) return launch<32, 2>(p, stream);
-  if (nchunks <= 32 * 8) return launch<32, 8>(p, stream);
-  if (nchunks <= 128 * 8) return launch<128, 8>(p, stream);
-  return launch<256, 8>(p, stream);
+  // How a row is laid over threads: the layout with the fewest idle chunks of
+  // 8, and of equals the one with fewer threads a row (shorter exchanges) unless
+  // that takes 8 chunks a thread (C = 5,120: 128 x 5 threads x chunks 394 us for
+  // 58,048 rows, 256 x 3 422; C = 13,824: 256 x 7 104 us for 12,345 rows, 512 x
+  // 4 118; C = 16,384: 512 x 4 94 us for 3,000 rows, 256 x 8 104; C = 2,048: 128
+  // x 2 18.5 us for 4,096 rows, 32 x 8 34). With fewer rows than would fill the
+  // GPU a row's latency counts, and more threads shorten it (200 rows of 5,120:
+  // 512 x 2 4.8 us, 128 x 5 6.3).
+  const int n = C / 8;
+  const bool plain = branch == nullptr && x_out == nullptr && norm_type == 2 && weight == nullptr && shift == nullptr;
+  const bool few = T <= 2 * num_sms;
+  int tpr = 0, cpt = 0, best = INT_MAX;
+  for (int t : {32, 128, 256, 512}) {
+    const int c = (n + t - 1) / t;
+    if (c > (few ? 2 : (t < 128 ? 4 : 7)) && t < 512) continue;
+    if (t * c < best) {
+      best = t * c;
+      tpr = t;
+      cpt = c;
+    }
+  }
+  switch (tpr * 8 + cpt) {
+#define PQK_LAYOUT(t, c) \
+  case t * 8 + c: return launch<t, c>(p, plain, stream)
+    PQK_LAYOUT(32, 1);
+    PQK_LAYOUT(32, 2);
+    PQK_LAYOUT(32, 3);
+    PQK_LAYOUT(32, 4);
+    PQK_LAYOUT(128, 1);
+    PQK_LAYOUT(128, 2);
+    PQK_LAYOUT(128, 3);
+    PQK_LAYOUT(128, 4);
+    PQK_LAYOUT(128, 5);
+    PQK_LAYOUT(128, 6);
+    PQK_LAYOUT(128, 7);
+    PQK_LAYOUT(256, 2);
+    PQK_LAYOUT(256, 4);
+    PQK_LAYOUT(256, 5);
+    PQK_LAYOUT(256, 6);
+    PQK_LAYOUT(256, 7);
+    PQK_LAYOUT(512, 2);
+    PQK_LAYOUT(512, 3);
+    PQK_LAYOUT(512, 4);
+#undef PQK_LAYOUT
+    default: return -1;  // unreachable: n <= 2048
+  }
 }
 
 }  // namespace pqk

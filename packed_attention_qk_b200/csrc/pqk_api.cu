@@ -440,7 +440,7 @@ int pqk_norm_modulate_i8(const void* x, int64_t x_stride_t, const void* branch, 
   if (int rc = check_device(&d)) return rc;
   return pqk::launch_norm_quant_i8(x, x_stride_t, branch, branch_stride_t, x_out, x_out_stride_t, h8, h8_stride_t,
                                    h_scale, weight, shift, scale, gate_res, vectors ? cu_seqlens : nullptr, B, T, C,
-                                   norm_type, eps, static_cast<cudaStream_t>(stream))
+                                   norm_type, eps, static_cast<cudaStream_t>(stream), d->num_sms)
              ? PQK_ERR_CUDA
              : PQK_OK;
 }

@@ -118,7 +118,7 @@ bool make_i8_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t c
 int launch_norm_quant_i8(const void* x, int64_t x_stride, const void* branch, int64_t branch_stride, void* x_out,
                          int64_t x_out_stride, void* h8, int64_t h8_stride, float* h_scale, const void* weight,
                          const float* shift, const float* scale, const float* gate_res, const int32_t* cu, int B,
-                         int64_t T, int C, int norm_type, float eps, cudaStream_t stream);
+                         int64_t T, int C, int norm_type, float eps, cudaStream_t stream, int num_sms);
 
 int launch_wait_selftest(int* status, long long timeout_ns, cudaStream_t stream);
 

@@ -87,6 +87,30 @@ def test_everything_on(C, norm):
     check(x, br, gate, w, shift, scale, cu, norm, 1e-5, x_out, h8, s)
 
 
+# many rows: a row is laid over fewer threads than in a call of a few
+@pytest.mark.parametrize("C", [256, 264, 520, 776, 1024, 1032, 2048, 2056, 3000, 4096, 5120, 5632, 6152, 7168, 7176, 8200,
+                               10248, 13824, 14344, 16384])
+def test_many_rows_of_every_layout(C):
+    torch = torch_cuda()
+    g = np.random.default_rng(C)
+    lens = [301, 0, 20, 1, 90]
+    T, B = sum(lens), len(lens)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    x, br = _bits(g.standard_normal((T, C)) - 0.25), _bits(g.standard_normal((T, C)))
+    w = _bits(g.uniform(0.5, 1.5, C))
+    gate, shift, scale = ((0.3 * g.standard_normal((B, C))).astype(np.float32) for _ in range(3))
+    for norm in (pqk.NORM_RMS, pqk.NORM_LAYER):
+        xo = torch.empty((T, C), dtype=torch.bfloat16, device="cuda")
+        _, h8, s = pqk.norm_modulate_i8(to_dev_bf16(x), branch=to_dev_bf16(br), gate_res=to_dev(gate),
+                                        weight=to_dev_bf16(w), shift=to_dev(shift), scale=to_dev(scale),
+                                        cu_seqlens=to_dev(cu), norm_type=norm, x_out=xo)
+        torch.cuda.synchronize()
+        check(x, br, gate, w, shift, scale, cu, norm, 1e-6, xo, h8, s)
+    x8, s = pqk.quantize_i8(to_dev_bf16(x))
+    torch.cuda.synchronize()
+    check(x, None, None, None, None, None, cu, pqk.NORM_NONE, 1.0, None, x8, s)
+
+
 @pytest.mark.parametrize("branch, gate, weight, mod", [
     (False, False, False, False), (True, False, False, False), (True, True, False, False), (False, False, True, False),
     (False, False, False, True), (True, False, True, True), (True, True, True, False)])
