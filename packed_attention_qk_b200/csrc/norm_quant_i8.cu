@@ -49,6 +49,7 @@ struct NormQuantParams {
   int C;
   int norm_type;
   float eps;
+  bool wide;  // shift, scale and gate_res start on 32-byte boundaries
 };
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -60,17 +61,26 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-// Streamed once: kept out of L1, which the modulation vectors use.
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+__device__ __forceinline__ uint4 ld16(const void* p) {
   uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p)
                : "memory");
   return v;
 }
 
-__device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
+// Eight entries of a request's vector, in one 32-byte load where the vectors
+// start on 32-byte boundaries: two 16-byte loads with 32 bytes between lanes
+// pass twice as many lines through L1 ([58,048, 5,120] with all vectors: 395 us
+// with the latter, 366 with the former).
+__device__ __forceinline__ void load8f(const float* p, bool wide, float (&f)[8]) {
+  if (wide) {
+    asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+        : "l"(p));
+    return;
+  }
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
@@ -92,13 +102,13 @@ __device__ __forceinline__ int find_segment(const int32_t* cu, int B, int64_t t)
 // the result. `slot`: kTpr / 32 words of shared memory used by this row only,
 // and by this exchange only until the row's next barrier.
 template <int kTpr, typename T, typename Op>
-__device__ __forceinline__ T row_reduce(T v, T* slot, int group, Op op) {
+__device__ __forceinline__ T row_reduce(T v, T* slot, Op op) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, off));
   if constexpr (kTpr > 32) {
     const int warp_in_row = (threadIdx.x % kTpr) >> 5;
     if ((threadIdx.x & 31) == 0) slot[warp_in_row] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kTpr) : "memory");
+    __syncthreads();  // such a row is a block of its own
     v = slot[0];
 #pragma unroll
     for (int i = 1; i < kTpr / 32; ++i) v = op(v, slot[i]);
@@ -113,14 +123,17 @@ struct MaxOp {
   __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
 
-// Threads per block, and the blocks per SM that the registers have to allow:
-// with 7 chunks a thread three blocks (80 registers) instead of two take a
-// [12,345, 13,824] quantisation from 127 to 104 us; elsewhere the compiler's
-// own choice is within 3 % of the best.
+// Threads per block: one row, or four of a warp each (blocks of two or four
+// rows of 128 threads leave more of an SM idle between rows: 364 and 491 us
+// where these take 348 for [58,048, 5,120]). And the blocks per SM that the
+// registers have to allow where the compiler would use more: 80 registers with
+// 7 chunks of x alone (12,345 rows of 13,824: 127 -> 104 us), 72 with 5 chunks
+// of everything (58,048 rows of 5,120: 357 -> 348 us, without the branch 250 ->
+// 233).
 template <int kTpr>
-constexpr int kBlock = kTpr < 256 ? 256 : kTpr;
+constexpr int kBlock = kTpr < 128 ? 128 : kTpr;
 template <int kTpr, int kCpt, bool kPlain>
-constexpr int kBlocksPerSm = kPlain && kTpr == 256 && kCpt >= 6 ? 3 : 1;
+constexpr int kBlocksPerSm = kPlain && kTpr == 256 && kCpt >= 6 ? 3 : (!kPlain && kTpr == 128 && kCpt == 5 ? 7 : 1);
 
 // kPlain: codes of x alone (no branch, norm or vectors), in fewer registers.
 template <int kTpr, int kCpt, bool kPlain>
@@ -145,13 +158,13 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
 #pragma unroll
     for (int i = 0; i < kCpt; ++i) {
       const int c = lane + i * kTpr;
-      xr[i] = c < nchunks ? ld_stream16(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
+      xr[i] = c < nchunks ? ld16(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
     }
     if (!kPlain && p.branch != nullptr) {
 #pragma unroll
       for (int i = 0; i < kCpt; ++i) {
         const int c = lane + i * kTpr;
-        br[i] = c < nchunks ? ld_stream16(p.branch + t * p.branch_stride + c * 8) : make_uint4(0, 0, 0, 0);
+        br[i] = c < nchunks ? ld16(p.branch + t * p.branch_stride + c * 8) : make_uint4(0, 0, 0, 0);
       }
     }
 #pragma unroll
@@ -162,7 +175,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
         float b[8], g[8];
         unpack8(br[i], b);
         if (p.gate_res != nullptr) {
-          load8f(p.gate_res + mod_row + c * 8, g);
+          load8f(p.gate_res + mod_row + c * 8, p.wide, g);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[i][e] = fmaf(g[e], b[e], v[i][e]);
         } else {
@@ -198,7 +211,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
       for (int i = 0; i < kCpt; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v[i][e];
-      mu = row_reduce<kTpr>(s, s_sum[group][0], group, AddOp()) * inv_c;
+      mu = row_reduce<kTpr>(s, s_sum[group][0], AddOp()) * inv_c;
     }
     // centred second moment (mu = 0 for RMS); elements past C stay 0
     float s2 = 0.f;
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
         }
       }
     }
-    s2 = row_reduce<kTpr>(s2, s_sum[group][1], group, AddOp()) * inv_c;
+    s2 = row_reduce<kTpr>(s2, s_sum[group][1], AddOp()) * inv_c;
     // squares past fp32's range: the row counts as not finite
     const float inv = s2 <= 3.402823466e38f ? 1.0f / sqrtf(s2 + p.eps) : __int_as_float(0x7fffffff);
 #pragma unroll
@@ -233,8 +246,8 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
       }
       if (!kPlain && p.shift != nullptr) {
         float sc[8], sh[8];
-        load8f(p.scale + mod_row + c * 8, sc);
-        load8f(p.shift + mod_row + c * 8, sh);
+        load8f(p.scale + mod_row + c * 8, p.wide, sc);
+        load8f(p.shift + mod_row + c * 8, p.wide, sh);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = fmaf(v[i][e], 1.0f + sc[e], sh[e]);
       }
@@ -242,7 +255,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
       for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
     }
   }
-  top = row_reduce<kTpr>(top, s_max[group], group, MaxOp());
+  top = row_reduce<kTpr>(top, s_max[group], MaxOp());
 
   const bool finite = top < 0x7f800000u;
   const float amax = __uint_as_float(top);
@@ -305,14 +318,16 @@ int launch_norm_quant_i8(const void* x, int64_t x_stride, const void* branch, in
   p.C = C;
   p.norm_type = norm_type;
   p.eps = eps;
+  p.wide = (reinterpret_cast<uintptr_t>(shift) | reinterpret_cast<uintptr_t>(scale) |
+            reinterpret_cast<uintptr_t>(gate_res)) % 32 == 0;
   // How a row is laid over threads: the layout with the fewest idle chunks of
   // 8, and of equals the one with fewer threads a row (shorter exchanges) unless
-  // that takes 8 chunks a thread (C = 5,120: 128 x 5 threads x chunks 394 us for
-  // 58,048 rows, 256 x 3 422; C = 13,824: 256 x 7 104 us for 12,345 rows, 512 x
-  // 4 118; C = 16,384: 512 x 4 94 us for 3,000 rows, 256 x 8 104; C = 2,048: 128
-  // x 2 18.5 us for 4,096 rows, 32 x 8 34). With fewer rows than would fill the
-  // GPU a row's latency counts, and more threads shorten it (200 rows of 5,120:
-  // 512 x 2 4.8 us, 128 x 5 6.3).
+  // that takes 8 chunks a thread. Measured at one stage of the kernel, threads x
+  // chunks: C = 5,120, 58,048 rows: 128 x 5 394 us, 256 x 3 422; C = 13,824,
+  // 12,345 rows: 256 x 7 104, 512 x 4 118; C = 16,384, 3,000 rows: 512 x 4 94,
+  // 256 x 8 104; C = 2,048, 4,096 rows: 128 x 2 18.5, 32 x 8 34. With fewer rows
+  // than would fill the GPU a row's latency counts, and more threads shorten it
+  // (200 rows of 5,120: 512 x 2 4.8 us, 128 x 5 6.3).
   const int n = C / 8;
   const bool plain = branch == nullptr && x_out == nullptr && norm_type == 2 && weight == nullptr && shift == nullptr;
   const bool few = T <= 2 * num_sms;
