@@ -134,7 +134,7 @@ def _check(fn: str, rc: int) -> None:
 def _stream(stream) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    torch = _torch or _load_torch()
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
@@ -152,6 +152,16 @@ def _token_stride(t, ndim: int) -> int:
     return t.stride(0)
 
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 class _Args:
     """Checks of one call's tensors: type, shape, unit stride inside a row,
     and the current CUDA device (the library launches on it). What a call
@@ -161,8 +171,7 @@ class _Args:
     __slots__ = ("fn", "torch", "dev")
 
     def __init__(self, fn: str):
-        import torch
-        self.fn, self.torch, self.dev = fn, torch, None
+        self.fn, self.torch, self.dev = fn, _torch or _load_torch(), None
 
     def fail(self, name: str, why: str):
         raise ValueError(f"{self.fn}: {name} {why}")
@@ -199,6 +208,13 @@ class _Args:
         """t must be `dtype`, of `shape` and contiguous inside a row (all
         dimensions but the first). Returns the row stride; for at most one row,
         whose stride means nothing, its length in whole 16-byte units."""
+        try:
+            if t.dtype is dtype and t.shape == shape and t.get_device() == self.dev and shape[0] > 1:
+                strides = t.stride()
+                if strides[-1] == 1 and (len(shape) == 2 or strides[1] == shape[2]):
+                    return strides[0]
+        except AttributeError:
+            self.fail(name, "is not a tensor")
         self._kind(name, t, dtype, shape)
         strides = t.stride()
         want = 1
@@ -233,29 +249,29 @@ def _requests(a: _Args, cu_seqlens, name: str = "cu_seqlens") -> int:
     return n - 1
 
 
-def _rows_i8(a: _Args, name: str, t, T: int, C: int, device):
-    """The int8 [T, C] tensor t, or a new one whose rows start on 16-byte
-    boundaries, and its row stride."""
+def _rows_i8(a: _Args, name: str, t, T: int, C: int, like):
+    """The int8 [T, C] tensor t, or a new one on like's device whose rows start
+    on 16-byte boundaries, and its row stride."""
     if t is not None:
         return t, a.rows(name, t, a.torch.int8, (T, C))
     wide = (C + 15) // 16 * 16
-    t = a.torch.empty((T, wide), dtype=a.torch.int8, device=device)
+    t = like.new_empty((T, wide), dtype=a.torch.int8)
     return (t if wide == C else t[:, :C]), wide
 
 
-def _floats(a: _Args, name: str, t, n: int, device):
+def _floats(a: _Args, name: str, t, n: int, like):
     """The fp32 [n] tensor t, or a new one."""
     if t is None:
-        return a.torch.empty(n, dtype=a.torch.float32, device=device)
+        return like.new_empty(n, dtype=a.torch.float32)
     a.whole(name, t, a.torch.float32, (n,))
     return t
 
 
-def _rows_bf16(a: _Args, name: str, t, shape, device):
+def _rows_bf16(a: _Args, name: str, t, shape, like):
     """The bf16 tensor t of `shape`, or a new one, and its row stride."""
     if t is not None:
         return t, a.rows(name, t, a.torch.bfloat16, shape)
-    t = a.torch.empty(shape, dtype=a.torch.bfloat16, device=device)
+    t = like.new_empty(shape, dtype=a.torch.bfloat16)
     return t, math.prod(shape[1:])
 
 
@@ -550,9 +566,8 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
     x, branch, x_out: bf16 [T, C] (rows may be strided; x_out may be x);
     weight bf16 [C]; gate_res, shift, scale fp32 [B, C]; cu_seqlens int32
     [B+1]. Returns (x_out or None, h8 int8 [T, C], h_scale fp32 [T])."""
-    import torch
     a = _Args("norm_modulate_i8")
-    bf16, f32 = torch.bfloat16, torch.float32
+    bf16, f32 = a.torch.bfloat16, a.torch.float32
     shape = a.first("x", x, bf16, 2)
     T, Cdim = shape
     x_stride = a.rows("x", x, bf16, shape)
@@ -567,8 +582,8 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
         a.whole("scale", scale, f32, (B, Cdim))
     if weight is not None:
         a.whole("weight", weight, bf16, (Cdim,))
-    h8, h8_stride = _rows_i8(a, "h8", h8, T, Cdim, x.device)
-    h_scale = _floats(a, "h_scale", h_scale, T, x.device)
+    h8, h8_stride = _rows_i8(a, "h8", h8, T, Cdim, x)
+    h_scale = _floats(a, "h_scale", h_scale, T, x)
     _check("pqk_norm_modulate_i8", lib().pqk_norm_modulate_i8(
         _ptr(x), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, _ptr(h8), h8_stride, _ptr(h_scale),
         _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim, norm_type, eps,
@@ -579,13 +594,13 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
 def quantize_i8(x, *, x8=None, scales=None, stream=None):
     """The rows of a bf16 tensor [T, C] as int8 codes with one scale per row
     (max |x| / 127). Returns (x8 int8 [T, C], scales fp32 [T])."""
-    import torch
     a = _Args("quantize_i8")
-    shape = a.first("x", x, torch.bfloat16, 2)
+    bf16 = a.torch.bfloat16
+    shape = a.first("x", x, bf16, 2)
     T, Cdim = shape
-    x_stride = a.rows("x", x, torch.bfloat16, shape)
-    x8, x8_stride = _rows_i8(a, "x8", x8, T, Cdim, x.device)
-    scales = _floats(a, "scales", scales, T, x.device)
+    x_stride = a.rows("x", x, bf16, shape)
+    x8, x8_stride = _rows_i8(a, "x8", x8, T, Cdim, x)
+    scales = _floats(a, "scales", scales, T, x)
     _check("pqk_quantize_i8", lib().pqk_quantize_i8(_ptr(x), x_stride, T, Cdim, _ptr(x8), x8_stride, _ptr(scales),
                                                      _stream(stream)))
     return x8, scales
@@ -612,14 +627,13 @@ def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None,
     [T, K], w8: int8 [N, K] (rows on 16-byte boundaries, as quantize_i8 and
     norm_modulate_i8 give them), a_scale fp32 [T], w_scale fp32 [N], x bf16
     [T, N], gate_res fp32 [B, N]. out (bf16) may be x (in place)."""
-    import torch
     a = _Args("linear_i8_gated_residual")
     T, K, N, a_stride, w_stride = _i8_operands(a, a8, a_scale, w8, w_scale)
     B = _requests(a, cu_seqlens)
-    x_stride = 0 if x is None else a.rows("x", x, torch.bfloat16, (T, N))
+    x_stride = 0 if x is None else a.rows("x", x, a.torch.bfloat16, (T, N))
     if gate_res is not None:
-        a.whole("gate_res", gate_res, torch.float32, (B, N))
-    out, out_stride = _rows_bf16(a, "out", out, (T, N), a8.device)
+        a.whole("gate_res", gate_res, a.torch.float32, (B, N))
+    out, out_stride = _rows_bf16(a, "out", out, (T, N), a8)
     _check("pqk_linear_i8_gated_residual", lib().pqk_linear_i8_gated_residual(
         _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(x), x_stride, _ptr(gate_res),
         _ptr(cu_seqlens), B, _ptr(out), out_stride, T, K, N, _stream(stream)))
@@ -635,7 +649,7 @@ def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
     F, odd = divmod(rows, 2)
     if odd:
         a.fail("w8", "has an odd number of rows")
-    act, act_stride = _rows_bf16(a, "act", act, (T, F), a8.device)
+    act, act_stride = _rows_bf16(a, "act", act, (T, F), a8)
     _check("pqk_linear_i8_swiglu", lib().pqk_linear_i8_swiglu(
         _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(act), act_stride, T, K, F,
         _stream(stream)))
@@ -654,9 +668,8 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     0 to at most Tq and Tk (rows behind the last request are left as they
     are). A request without keys gives o = 0, lse = -inf. Returns (o, lse
     fp32 [H, Tq] or None)."""
-    import torch
     a = _Args("varlen_cross_attn_fwd")
-    bf16 = torch.bfloat16
+    torch, bf16 = a.torch, a.torch.bfloat16
     shape = a.first("q", q, bf16, 3)
     Tq, H, D = shape
     q_stride = a.rows("q", q, bf16, shape)
@@ -670,13 +683,13 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     B = _requests(a, cu_seqlens_q, "cu_seqlens_q")
     a.whole("cu_seqlens_k", cu_seqlens_k, torch.int32, (B + 1,))
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
-    o, o_stride = _rows_bf16(a, "o", o, shape, q.device)
+    o, o_stride = _rows_bf16(a, "o", o, shape, q)
     if lse is not None:
         a.whole("lse", lse, torch.float32, (H, Tq))
     elif want_lse:
-        lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((H, Tq), dtype=torch.float32)
     if workspace is None:
-        workspace = torch.empty(varlen_cross_attn_workspace_size(B, D), dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(varlen_cross_attn_workspace_size(B, D), dtype=torch.uint8)
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != q.device:
         a.fail("workspace", f"is not a contiguous tensor on {q.device}")
     _check("pqk_varlen_cross_attn_fwd", lib().pqk_varlen_cross_attn_fwd(
