@@ -14,7 +14,13 @@
 // row (kind::i8, int32 accumulation, which is exact); the accumulator times
 // the two scales takes the place of (A W^T) above. A 128-byte swizzle row then
 // holds 128 K positions instead of 64, and everything between the tensor maps
-// and the accumulator is the same.
+// and the accumulator is the same. A tile's products then take half the time
+// (512 cycles a stage), less than the epilogue above with its one row a lane
+// needs for K below about 5,000 (16,384 tokens, K = 1,024, N = 2,048 with the
+// residual: 14 us a tile against 2.2), so kI8 has an epilogue of its own: eight
+// warps, 32 rows x 128 columns each, whose accumulators go through shared memory
+// so that x is read and the output written 64 bytes of a row at a time; x and
+// the scales are loaded before the accumulator is waited for.
 //
 // A: [T, K] bf16 (token stride a_stride), W: [N, K] bf16 (out x in). fp32
 // accumulation in tensor memory, epilogue arithmetic in fp32, bf16 output
@@ -69,16 +75,22 @@ constexpr int kRowBytes = 128; // K per stage: one 128-byte swizzle row, 64 bf16
 constexpr int kBoxRows = 128;  // W rows per CTA and stage
 constexpr int kAccCols = 256;  // fp32 accumulator columns per tile = MMA N
 constexpr int kStages = 6;
-constexpr int kThreads = 192;
+template <bool kI8>
+constexpr int kThreads = kI8 ? 320 : 192;
+template <bool kI8>
+constexpr int kEpilogueWarps = kI8 ? 8 : 4;  // per CTA
 constexpr int kGroupM = 8;     // raster: pair M tiles per group
 constexpr uint32_t kABytes = kBM * kRowBytes;        // 16 KB
 constexpr uint32_t kBBytes = kBoxRows * kRowBytes;   // 16 KB
 constexpr uint32_t kPairStageBytes = 2 * (kABytes + kBBytes);
 
+template <bool kI8>
 struct Layout {
   static constexpr int kAOff = 0;
   static constexpr int kBOff = kStages * kABytes;
-  static constexpr int kBarOff = kBOff + kStages * kBBytes;
+  // kI8: 32 rows x 32 accumulators for each epilogue warp
+  static constexpr int kOutOff = kBOff + kStages * kBBytes;
+  static constexpr int kBarOff = kOutOff + (kI8 ? kEpilogueWarps<kI8> * 4096 : 0);
   // full[S], empty[S], acc_full[2], acc_empty[2], drain
   static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
@@ -140,30 +152,132 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// kCount consecutive accumulator columns as floats: as they are, or int32 sums
-// times the token's and the columns' scales (ws: the first column's).
-template <bool kI8, int kCount>
-__device__ __forceinline__ void acc_values(const uint32_t* acc, float row_scale, const float* ws, float (&o)[kCount]) {
-  if constexpr (kI8) {
+// Four neighbouring int32 sums of a token times its scale and theirs.
+__device__ __forceinline__ void scaled4(int4 sum, float row_scale, float4 w, float (&y)[4]) {
+  y[0] = __int2float_rn(sum.x) * row_scale * w.x;
+  y[1] = __int2float_rn(sum.y) * row_scale * w.y;
+  y[2] = __int2float_rn(sum.z) * row_scale * w.z;
+  y[3] = __int2float_rn(sum.w) * row_scale * w.w;
+}
+
+// The kI8 epilogue of one warp: 32 rows from row0 on, its half of the tile's
+// columns (t_acc: the accumulator at the warp's rows, `half` which half). Lane
+// l works on rows row0 + 4 i + l / 8 and the 4 columns from 4 (l % 8) on of
+// each chunk of 32. ready() waits for the accumulator and is false when the
+// kernel aborts; release() is called once the accumulator has been read.
+template <int kEpi, typename Ready, typename Release>
+__device__ __forceinline__ bool store_rows_i8(const Params& p, uint32_t t_acc, uint32_t stage, int64_t row0, int tile_n,
+                                              int half, Ready ready, Release release) {
+  constexpr int kChunks = kEpi == kEpiSwiglu ? 2 : 4;  // of 32 output columns
+  const int lane = threadIdx.x & 31;
+  const int sub = lane >> 3;
+  const int piece = lane & 7;
+  const int col0 = kEpi == kEpiSwiglu ? tile_n * kBoxRows + half * 64 + piece * 4
+                                      : tile_n * kAccCols + half * 128 + piece * 4;
+  // everything but the accumulator, before it is waited for
+  float row_scale[8];
+  float4 w[kChunks], w_up[kEpi == kEpiSwiglu ? kChunks : 1];
+  uint2 x[kEpi == kEpiGatedResidual ? kChunks : 1][8];
 #pragma unroll
-    for (int e = 0; e < kCount; e += 4) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(ws + e));
-      o[e] = __int2float_rn(static_cast<int>(acc[e])) * row_scale * w.x;
-      o[e + 1] = __int2float_rn(static_cast<int>(acc[e + 1])) * row_scale * w.y;
-      o[e + 2] = __int2float_rn(static_cast<int>(acc[e + 2])) * row_scale * w.z;
-      o[e + 3] = __int2float_rn(static_cast<int>(acc[e + 3])) * row_scale * w.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < kCount; ++e) o[e] = __uint_as_float(acc[e]);
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = row0 + 4 * i + sub;
+    row_scale[i] = row < p.T ? __ldg(p.a_scale + row) : 0.f;
   }
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int col = col0 + c * 32;
+    const bool in = col < p.N;
+    w[c] = in ? __ldg(reinterpret_cast<const float4*>(p.w_scale + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (kEpi == kEpiSwiglu)
+      w_up[c] = in ? __ldg(reinterpret_cast<const float4*>(p.w_scale + p.N + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (kEpi == kEpiGatedResidual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t row = row0 + 4 * i + sub;
+        x[c][i] = in && row < p.T ? *reinterpret_cast<const uint2*>(p.x + row * p.x_stride + col) : make_uint2(0u, 0u);
+      }
+    }
+  }
+  // the request of the warp's rows, if it is one
+  int request = 0;
+  bool one_request = true;
+  if constexpr (kEpi == kEpiGatedResidual) {
+    const int64_t last = row0 + 31 < p.T ? row0 + 31 : p.T - 1;
+    request = request_of(p.cu, p.B, row0 < p.T ? row0 : p.T - 1);
+    one_request = request == request_of(p.cu, p.B, last);
+  }
+  if (!ready()) return false;
+  const uint32_t put = stage + lane * 128;
+  // 32 accumulators of this lane's row (tensor-memory lane) to shared memory,
+  // 16-byte piece ^ row in the row's 128 bytes so that neither this nor the
+  // reads below meet in a bank
+  auto transpose = [&](int acc_col) {
+    uint32_t v[32];
+    tmem_ld_x32(t_acc + acc_col, v);
+    __syncwarp();  // the chunk before has been read
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      st_shared16(put + ((c ^ (lane & 7)) * 16), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    __syncwarp();
+  };
+  auto sums = [&](int i) {
+    const int row = 4 * i + sub;
+    return ld_shared16(stage + row * 128 + ((piece ^ (row & 7)) * 16));
+  };
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const int col = col0 + c * 32;
+    const bool in = col < p.N;
+    float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (kEpi == kEpiGatedResidual) {
+      if (in && one_request)
+        g = __ldg(reinterpret_cast<const float4*>(p.gate_res + static_cast<int64_t>(request) * p.N + col));
+    }
+    int4 gate_sums[kEpi == kEpiSwiglu ? 8 : 1];
+    if constexpr (kEpi == kEpiSwiglu) {
+      transpose(half * 64 + c * 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) gate_sums[i] = sums(i);
+      transpose(kBoxRows + half * 64 + c * 32);
+    } else {
+      transpose(half * 128 + c * 32);
+    }
+    if (c + 1 == kChunks) release();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + 4 * i + sub;
+      float y[4];
+      if constexpr (kEpi == kEpiSwiglu) {
+        float up[4];
+        scaled4(gate_sums[i], row_scale[i], w[c], y);
+        scaled4(sums(i), row_scale[i], w_up[c], up);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = silu_mul(y[e], up[e]);
+      } else {
+        scaled4(sums(i), row_scale[i], w[c], y);
+      }
+      if (!in || row >= p.T) continue;
+      if constexpr (kEpi == kEpiGatedResidual) {
+        if (!one_request)
+          g = __ldg(reinterpret_cast<const float4*>(
+              p.gate_res + static_cast<int64_t>(request_of(p.cu, p.B, row)) * p.N + col));
+        y[0] = fmaf(g.x, y[0], bf16_lo(x[c][i].x));
+        y[1] = fmaf(g.y, y[1], bf16_hi(x[c][i].x));
+        y[2] = fmaf(g.z, y[2], bf16_lo(x[c][i].y));
+        y[3] = fmaf(g.w, y[3], bf16_hi(x[c][i].y));
+      }
+      *reinterpret_cast<uint2*>(p.out + row * p.out_stride + col) =
+          make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    }
+  }
+  return true;
 }
 
 template <int kEpi, bool kI8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<kI8>, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b0,
                        const __grid_constant__ CUtensorMap tm_b1, const Params p) {
-  using L = Layout;
+  using L = Layout<kI8>;
   constexpr int kBlockK = kI8 ? kRowBytes : kRowBytes / 2;  // K positions per stage
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_addr(smem_raw);
@@ -198,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full(i), 1);
-      mbar_init(acc_empty(i), 2 * 4);  // one arrive per epilogue warp of each CTA
+      mbar_init(acc_empty(i), 2 * kEpilogueWarps<kI8>);  // one arrive per epilogue warp of each CTA
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -292,11 +406,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) raise_abort();
     }
   } else {
-    // ------------------------------------------------ epilogue warps 2-5 (both CTAs)
+    // ------------------------------------------------ epilogue warps 2-5, or 2-9 (both CTAs)
     const int quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     int tcount = 0;
     bool ok = true;
+    if constexpr (kI8) {
+      const uint32_t stage = base + L::kOutOff + (warp - 2) * 4096;
+      for (int tile = pair; tile < total && ok; tile += npairs, ++tcount) {
+        const TileCoord tc = tile_coord(tile, p.m_pairs, p.n_tiles);
+        const int acc = tcount & 1;
+        auto ready = [&]() {
+          const bool got = __all_sync(
+              0xffffffffu, mbar_wait(acc_full(acc), static_cast<uint32_t>(tcount >> 1) & 1, abort_flag, p.timeout_ns));
+          if (!got) return false;
+          // the even CTA's MMAs wrote both CTAs' accumulators: tell the odd CTA
+          if (even && warp == 2 && lane == 0) arrive_remote(in_cta(acc_full(acc), 1));
+          tc_fence_after_sync();
+          return true;
+        };
+        auto release = [&]() {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive_remote(in_cta(acc_empty(acc), 0));
+        };
+        ok = store_rows_i8<kEpi>(p, tmem + lane_off + static_cast<uint32_t>(acc * kAccCols), stage,
+                                 static_cast<int64_t>(tc.m) * 2 * kBM + rank * kBM + quarter * 32, tc.n,
+                                 (warp - 2) >> 2, ready, release);
+      }
+    } else
     for (int tile = pair; tile < total; tile += npairs, ++tcount) {
       const TileCoord tc = tile_coord(tile, p.m_pairs, p.n_tiles);
       const int acc = tcount & 1;
@@ -310,7 +448,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = row < p.T;
       const uint32_t t_acc = tmem + lane_off + static_cast<uint32_t>(acc * kAccCols);
       __nv_bfloat16* dst = p.out + (row_ok ? row : 0) * p.out_stride;
-      const float row_scale = kI8 && row_ok ? __ldg(p.a_scale + row) : 1.0f;
       if constexpr (kEpi == kEpiSwiglu) {
         const int f0 = tc.n * kBoxRows;
 #pragma unroll 1
@@ -323,14 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; c += 8) {
               const int col = f0 + c0 + c;
               if (col < p.N) {
-                float gv[8], uv[8];
-                acc_values<kI8>(g + c, row_scale, p.w_scale + col, gv);
-                acc_values<kI8>(u + c, row_scale, p.w_scale + p.N + col, uv);
                 uint4 v;
-                v.x = pack_bf16x2(silu_mul(gv[0], uv[0]), silu_mul(gv[1], uv[1]));
-                v.y = pack_bf16x2(silu_mul(gv[2], uv[2]), silu_mul(gv[3], uv[3]));
-                v.z = pack_bf16x2(silu_mul(gv[4], uv[4]), silu_mul(gv[5], uv[5]));
-                v.w = pack_bf16x2(silu_mul(gv[6], uv[6]), silu_mul(gv[7], uv[7]));
+                v.x = pack_bf16x2(silu_mul(__uint_as_float(g[c]), __uint_as_float(u[c])),
+                                  silu_mul(__uint_as_float(g[c + 1]), __uint_as_float(u[c + 1])));
+                v.y = pack_bf16x2(silu_mul(__uint_as_float(g[c + 2]), __uint_as_float(u[c + 2])),
+                                  silu_mul(__uint_as_float(g[c + 3]), __uint_as_float(u[c + 3])));
+                v.z = pack_bf16x2(silu_mul(__uint_as_float(g[c + 4]), __uint_as_float(u[c + 4])),
+                                  silu_mul(__uint_as_float(g[c + 5]), __uint_as_float(u[c + 5])));
+                v.w = pack_bf16x2(silu_mul(__uint_as_float(g[c + 6]), __uint_as_float(u[c + 6])),
+                                  silu_mul(__uint_as_float(g[c + 7]), __uint_as_float(u[c + 7])));
                 *reinterpret_cast<uint4*>(dst + col) = v;
               }
             }
@@ -354,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int col = n0 + c0 + c;
               if (col < p.N) {
                 float o[8];
-                acc_values<kI8>(y + c, row_scale, p.w_scale + col, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __uint_as_float(y[c + e]);
                 if constexpr (kEpi == kEpiGatedResidual) {
                   const uint4 xv = ld_nc16(xrow + col);
                   const float4 g0 = __ldg(reinterpret_cast<const float4*>(grow + col));
@@ -457,7 +596,7 @@ int resident_pairs(cudaLaunchConfig_t* cfg) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
   if (pairs[dev] == 0) {
     if (cudaFuncSetAttribute(linear_pair_kernel<kEpi, kI8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout::kAlloc) != cudaSuccess)
+                             Layout<kI8>::kAlloc) != cudaSuccess)
       return -1;
     int n = 0;
     cfg->gridDim = dim3(2, 1, 1);
@@ -476,8 +615,8 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Layout::kAlloc;
+  cfg.blockDim = dim3(kThreads<kI8>, 1, 1);
+  cfg.dynamicSmemBytes = Layout<kI8>::kAlloc;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
