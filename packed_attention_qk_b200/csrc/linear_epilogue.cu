@@ -79,7 +79,11 @@ template <bool kI8>
 constexpr int kThreads = kI8 ? 320 : 192;
 template <bool kI8>
 constexpr int kEpilogueWarps = kI8 ? 8 : 4;  // per CTA
-constexpr int kGroupM = 8;     // raster: pair M tiles per group
+// Raster: pair M tiles per group. int8 rows are half as long, so twice as many
+// stay in L2 while W passes by (58,048 x 5,120 -> SwiGLU 13,824: 6.1-6.5 ms with
+// 8, 5.8-5.9 with 16; with 32 layers of K = 13,824 lose 8 %).
+template <bool kI8>
+constexpr int kGroupM = kI8 ? 16 : 8;
 constexpr uint32_t kABytes = kBM * kRowBytes;        // 16 KB
 constexpr uint32_t kBBytes = kBoxRows * kRowBytes;   // 16 KB
 constexpr uint32_t kPairStageBytes = 2 * (kABytes + kBBytes);
@@ -123,11 +127,12 @@ struct TileCoord {
   int m;
   int n;
 };
+template <bool kI8>
 __device__ __forceinline__ TileCoord tile_coord(int i, int m_tiles, int n_tiles) {
-  const int group_tiles = kGroupM * n_tiles;
+  const int group_tiles = kGroupM<kI8> * n_tiles;
   const int g = i / group_tiles;
-  const int first_m = g * kGroupM;
-  const int gm = min(kGroupM, m_tiles - first_m);
+  const int first_m = g * kGroupM<kI8>;
+  const int gm = min(kGroupM<kI8>, m_tiles - first_m);
   const int local = i - g * group_tiles;
   TileCoord c;
   c.m = first_m + local % gm;
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(kThreads<kI8>, 1)
       bool ok = true;
       const CUtensorMap* mb = (kEpi == kEpiSwiglu && !even) ? &tm_b1 : &tm_b0;
       for (int tile = pair; tile < total && ok; tile += npairs) {
-        const TileCoord tc = tile_coord(tile, p.m_pairs, p.n_tiles);
+        const TileCoord tc = tile_coord<kI8>(tile, p.m_pairs, p.n_tiles);
         const int arow = tc.m * 2 * kBM + static_cast<int>(rank) * kBM;
         const int brow = kEpi == kEpiSwiglu ? tc.n * kBoxRows : tc.n * kAccCols + static_cast<int>(rank) * kBoxRows;
         for (int kb = 0; kb < p.n_kb; ++kb) {
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kThreads<kI8>, 1)
     if constexpr (kI8) {
       const uint32_t stage = base + L::kOutOff + (warp - 2) * 4096;
       for (int tile = pair; tile < total && ok; tile += npairs, ++tcount) {
-        const TileCoord tc = tile_coord(tile, p.m_pairs, p.n_tiles);
+        const TileCoord tc = tile_coord<kI8>(tile, p.m_pairs, p.n_tiles);
         const int acc = tcount & 1;
         auto ready = [&]() {
           const bool got = __all_sync(
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kThreads<kI8>, 1)
       }
     } else
     for (int tile = pair; tile < total; tile += npairs, ++tcount) {
-      const TileCoord tc = tile_coord(tile, p.m_pairs, p.n_tiles);
+      const TileCoord tc = tile_coord<kI8>(tile, p.m_pairs, p.n_tiles);
       const int acc = tcount & 1;
       const uint32_t use = static_cast<uint32_t>(tcount >> 1);
       ok = __all_sync(0xffffffffu, mbar_wait(acc_full(acc), use & 1, abort_flag, p.timeout_ns));
@@ -696,13 +701,30 @@ int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_s
                      int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride, const float* gate_res,
                      const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K, int N, int* status,
                      long long timeout_ns, cudaStream_t stream, int num_sms) {
-  const int n_kb = (K + kRowBytes - 1) / kRowBytes;
-  const int64_t pair_tiles = (T + 2 * kBM - 1) / (2 * kBM) * ((N + kAccCols - 1) / kAccCols);
-  if (pair_tiles <= num_sms / 4) {
-    const int token_tile = T <= 32 ? 32 : (T <= 64 ? 64 : 128);
-    const int64_t tiles = (T + token_tile - 1) / token_tile * ((N + 127) / 128) * (epi == kEpiSwiglu ? 2 : 1);
+  // Which kernel. Few tokens are W's bytes: the kernel with W on the M side is
+  // ahead whatever N is (T = 32, K = 5,120 -> SwiGLU 13,824: 27.7 against 35.7
+  // us). More tokens are not, but leave most SMs without a tile of 256 x 256:
+  // up to a tile for every third pair of SMs the smaller tiles with K split
+  // over a cluster win (256 x 5,120 x 5,120, 20 tiles: 15.9 against 18.4 us;
+  // 512 x 2,048 x 2,048, 16 tiles: 9.2 / 11.4; 1,024 x 2,048 x 2,048, 32
+  // tiles: 11.7 / 11.6; 389 x 2,048 x 5,120, 40 tiles: 12.2 / 11.7).
+  const int w_rows = epi == kEpiSwiglu ? 2 * N : N;
+  const int64_t pair_tiles = ((T + 255) / 256) * ((static_cast<int64_t>(w_rows) + 255) / 256);
+  if (T <= 64 || pair_tiles <= num_sms / 6) {
+    // Tokens per tile: 64 while its tiles leave room for two K parts in the two
+    // CTAs that an SM holds, else 128, which reads W half as often (256 x 5,120
+    // x 5,120: 128 tokens, 3 parts 15.9 us, 64 tokens 18.1; 192 tokens: 15.0 /
+    // 14.4). K parts: as many as fit at once, more than four only where each
+    // still has eight blocks of K (T = 1, 5,120 x 5,120: 4 parts 9.3 us, 6 9.7,
+    // 1 14.9; 8 x 13,824 x 128: 8 parts 7.8, 4 10.5).
+    const int n_kb = (K + kRowBytes - 1) / kRowBytes;
+    const int slots = 2 * num_sms;
+    const int64_t w_tiles = (static_cast<int64_t>(w_rows) + 127) / 128;
+    const int token_tile = T <= 32 ? 32 : ((T + 63) / 64 * w_tiles * 2 <= slots || T <= 64 ? 64 : 128);
+    const int64_t tiles = (T + token_tile - 1) / token_tile * w_tiles;
     int split = 1;
-    while (split < 8 && 2 * split <= n_kb && tiles * split * 2 <= 2 * num_sms) split *= 2;
+    for (int s : {2, 3, 4, 6, 8})
+      if (tiles * s <= slots && s <= n_kb && (s <= 4 || n_kb >= 8 * s)) split = s;
     return launch_linear_i8_few(epi, a8, a_stride, a_scale, w8, w_stride, w_scale, x, x_stride, gate_res, cu, B, out,
                                 out_stride, T, K, N, token_tile, split, status, timeout_ns, stream);
   }

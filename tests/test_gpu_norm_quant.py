@@ -149,6 +149,30 @@ def test_strides_in_place_and_guard_bytes():
     assert torch.isnan(xd.as_strided((T, 24), (C + 24, 1), C)).all()
 
 
+def test_vectors_on_16_but_not_32_byte_boundaries():
+    torch = torch_cuda()
+    g = np.random.default_rng(15)
+    lens, C = [70, 400], 1040
+    T, cu = sum(lens), np.array([0, 70, 470], np.int32)
+    x, br = _bits(g.standard_normal((T, C))), _bits(g.standard_normal((T, C)))
+    vec = [(0.3 * g.standard_normal((2, C))).astype(np.float32) for _ in range(3)]
+    flat = torch.empty(3 * (2 * C + 4), device="cuda")
+    views = []
+    for i, v in enumerate(vec):
+        t = flat[i * (2 * C + 4) + 4:][:2 * C].view(2, C)
+        t.copy_(to_dev(v))
+        views.append(t)
+    assert any(t.data_ptr() % 32 for t in views)
+    xo = torch.empty((T, C), dtype=torch.bfloat16, device="cuda")
+    args = dict(branch=to_dev_bf16(br), cu_seqlens=to_dev(cu), x_out=xo)
+    _, h8, s = pqk.norm_modulate_i8(to_dev_bf16(x), gate_res=views[0], shift=views[1], scale=views[2], **args)
+    torch.cuda.synchronize()
+    check(x, br, vec[0], None, vec[1], vec[2], cu, 0, 1e-6, xo, h8, s)
+    again = pqk.norm_modulate_i8(to_dev_bf16(x), gate_res=to_dev(vec[0]), shift=to_dev(vec[1]), scale=to_dev(vec[2]),
+                                 **args)
+    assert torch.equal(again[1], h8) and torch.equal(again[2], s)
+
+
 def test_extreme_rows():
     """Zero rows, rows of one value, the smallest and largest bf16 numbers, rows whose halves differ by 2^120, and
     values next to ties: the plain quantisation."""
