@@ -611,10 +611,9 @@ int resident_pairs(cudaLaunchConfig_t* cfg) {
   return pairs[dev];
 }
 
-template <int kEpi, bool kI8>
-int launch(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const Params& p,
-           cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
+// The launch configuration of a pair kernel but for its grid; attr: room for one.
+template <bool kI8>
+cudaLaunchConfig_t pair_config(cudaLaunchAttribute* attr, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
@@ -625,6 +624,14 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int kEpi, bool kI8>
+int launch(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const Params& p,
+           cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pair_config<kI8>(attr, stream);
   const int max_pairs = resident_pairs<kEpi, kI8>(&cfg);
   if (max_pairs < 1) return -1;
   const int tiles = p.m_pairs * p.n_tiles;
@@ -693,6 +700,27 @@ int launch_linear(int epi, const void* a, int64_t a_stride, const void* w, const
                      status, timeout_ns, stream);
 }
 
+namespace {
+
+// The settings of every kernel that an int8 call may choose, on the first call
+// on a device: a later one, of other sizes, may be under capture.
+bool prepare_i8(cudaStream_t stream) {
+  static int done[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (!done[dev]) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pair_config<true>(attr, stream);
+    if (resident_pairs<kEpiNone, true>(&cfg) < 1 || resident_pairs<kEpiGatedResidual, true>(&cfg) < 1 ||
+        resident_pairs<kEpiSwiglu, true>(&cfg) < 1 || !prepare_linear_i8_few())
+      return false;
+    done[dev] = 1;
+  }
+  return true;
+}
+
+}  // namespace
+
 bool make_i8_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
   return make_rows_map(map, ptr, rows, cols, stride, box_rows, true);
 }
@@ -701,6 +729,7 @@ int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_s
                      int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride, const float* gate_res,
                      const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T, int K, int N, int* status,
                      long long timeout_ns, cudaStream_t stream, int num_sms) {
+  if (!prepare_i8(stream)) return -1;
   // Which kernel. Few tokens are W's bytes: the kernel with W on the M side is
   // ahead whatever N is (T = 32, K = 5,120 -> SwiGLU 13,824: 27.7 against 35.7
   // us). More tokens are not, but leave most SMs without a tile of 256 x 256:

@@ -283,17 +283,18 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <int kNT, int kEpi>
+bool prepare() {
+  return cudaFuncSetAttribute(linear_few_kernel<kNT, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Layout<kNT>::kAlloc) == cudaSuccess;
+}
+template <int kNT>
+bool prepare_epis() {
+  return prepare<kNT, kEpiNone>() && prepare<kNT, kEpiGatedResidual>() && prepare<kNT, kEpiSwiglu>();
+}
+
+template <int kNT, int kEpi>
 int launch(const CUtensorMap& tw0, const CUtensorMap& tw1, const CUtensorMap& ta, const Params& p, int split,
            cudaStream_t stream) {
-  static int done[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(linear_few_kernel<kNT, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<kNT>::kAlloc) != cudaSuccess)
-      return -1;
-    done[dev] = 1;
-  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(split);
@@ -321,6 +322,8 @@ int launch_epi(int epi, const CUtensorMap& tw0, const CUtensorMap& tw1, const CU
 }
 
 }  // namespace
+
+bool prepare_linear_i8_few() { return prepare_epis<32>() && prepare_epis<64>() && prepare_epis<128>(); }
 
 int launch_linear_i8_few(int epi, const void* a8, int64_t a_stride, const float* a_scale, const void* w8,
                          int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride,

@@ -100,7 +100,9 @@ int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_s
 
 // The same with W's rows as the MMA's M side and tiles of 32, 64 or 128 tokens,
 // the K range of a tile split over the CTAs of a cluster (1 to 8, at most the
-// number of 128-byte K blocks).
+// number of 128-byte K blocks). prepare_linear_i8_few sets the kernels' shared-
+// memory attributes on the current device; call it before the first launch.
+bool prepare_linear_i8_few();
 int launch_linear_i8_few(int epi, const void* a8, int64_t a_stride, const float* a_scale, const void* w8,
                          int64_t w_stride, const float* w_scale, const void* x, int64_t x_stride,
                          const float* gate_res, const int32_t* cu, int B, void* out, int64_t out_stride, int64_t T,

@@ -1918,7 +1918,6 @@ size_t cross_sched_bytes(int B) { return (cross_sched_words(B) * sizeof(int32_t)
 template <int D>
 int launch_cross(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, int B,
                  int grid, bool may_cut, cudaStream_t stream) {
-  if (!set_smem_attr<D, false, false, false, true>()) return -1;
   // The attention kernel sets itself up while the schedule is still being
   // built (programmatic dependent launch) and waits for it where it first
   // needs it.
@@ -1963,6 +1962,10 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
                              cudaStream_t stream, int num_sms) {
   CUtensorMap tq, tk, tv;
   // without any key there is nothing to map: the maps are never read then
+  // all settings on the first call on a device: a later one, of other sizes, may be under capture
+  if (!set_smem_attr<64, false, false, false, true>() || !set_smem_attr<128, false, false, false, true>() ||
+      !set_schedule_smem_attr<true>())
+    return -1;
   const int group = H / Hkv;
   // heads of one key head in one unit. Past 32 of them a query tile's 128 rows
   // may be a quarter empty (128 mod pack), and K and V are read 32 times less
@@ -1977,7 +1980,6 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   int sort_n = 1;
   while (sort_n < B) sort_n <<= 1;
   const size_t sched_smem = B <= kSortLimit ? static_cast<size_t>(sort_n) * 8 : 0;
-  if (sched_smem > 48 * 1024 && !set_schedule_smem_attr<true>()) return -1;
   if (B <= kWarpRequests)
     build_cross_schedule_warp_kernel<<<1, 32, 0, stream>>>(cu_q, cu_k, B, Tq, Tk, H / pack, 2 * tile_q, sched, status);
   else

@@ -238,6 +238,17 @@ class _Args:
             self.fail(name, f"is on {t.device}, not on cuda:{self.dev}")
 
 
+def _used_on(a: _Args, stream, *tensors) -> None:
+    """Tensors that a call allocated (on the current stream's account) and used
+    on a stream of the caller's choice: their memory is not handed out again
+    before that stream is through with it."""
+    if stream is not None:
+        s = a.torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
 def _requests(a: _Args, cu_seqlens, name: str = "cu_seqlens") -> int:
     """The number of requests of a cu_seqlens (0 for None)."""
     if cu_seqlens is None:
@@ -588,6 +599,7 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
         _ptr(x), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, _ptr(h8), h8_stride, _ptr(h_scale),
         _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim, norm_type, eps,
         _stream(stream)))
+    _used_on(a, stream, h8, h_scale)
     return x_out, h8, h_scale
 
 
@@ -603,6 +615,7 @@ def quantize_i8(x, *, x8=None, scales=None, stream=None):
     scales = _floats(a, "scales", scales, T, x)
     _check("pqk_quantize_i8", lib().pqk_quantize_i8(_ptr(x), x_stride, T, Cdim, _ptr(x8), x8_stride, _ptr(scales),
                                                      _stream(stream)))
+    _used_on(a, stream, x8, scales)
     return x8, scales
 
 
@@ -637,6 +650,7 @@ def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None,
     _check("pqk_linear_i8_gated_residual", lib().pqk_linear_i8_gated_residual(
         _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(x), x_stride, _ptr(gate_res),
         _ptr(cu_seqlens), B, _ptr(out), out_stride, T, K, N, _stream(stream)))
+    _used_on(a, stream, out)
     return out
 
 
@@ -653,6 +667,7 @@ def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
     _check("pqk_linear_i8_swiglu", lib().pqk_linear_i8_swiglu(
         _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(act), act_stride, T, K, F,
         _stream(stream)))
+    _used_on(a, stream, act)
     return act
 
 
@@ -696,6 +711,7 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), q_stride, k_stride, v_stride, o_stride, _ptr(cu_seqlens_q),
         _ptr(cu_seqlens_k), B, Tq, Tk, H, Hkv, D, scale, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+    _used_on(a, stream, o, lse, workspace)
     return o, lse
 
 
