@@ -38,7 +38,8 @@
 //   warp 1      allocates the tensor memory of the pair; in the even CTA
 //               issues the MMAs and commits stage releases and finished
 //               accumulators to its own barriers.
-//   warps 2-5   epilogue in each CTA: 32 token rows per warp, 32 columns of
+//   warps 2-5   (kI8: 2-9, two per 32 rows, see below)
+//               epilogue in each CTA: 32 token rows per warp, 32 columns of
 //               the accumulator at a time, the gated residual or SwiGLU, 16-
 //               byte stores; one release per warp to the even CTA's MMA
 //               thread. The even CTA passes "accumulator ready" on to the odd

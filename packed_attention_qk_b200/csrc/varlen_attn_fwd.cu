@@ -142,7 +142,9 @@ constexpr int kSlabBytes = 128 * 128;      // 128 rows x 64 bf16 (one 128-byte s
 // tile wt + 1 only once the Q K^T products of tile wt are complete, and the
 // MMA thread starts tile wt + 1 only after the softmax warps have handed over
 // the last P of tile wt, so the producer is at most two tiles ahead of the
-// softmax warps: at most three slots are live.
+// softmax warps: at most three slots are live. Cross-attention may issue the
+// next unit's first S0 before the last P1 of the current one, so there the
+// producer can be three units ahead of the second softmax group: all four.
 constexpr int kWorkSlots = 4;
 
 template <int D, bool kPair = false, bool kCross = false>
