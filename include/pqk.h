@@ -476,8 +476,10 @@ PQK_API int pqk_linear_swiglu(const void* a, int64_t a_stride_t, const void* w1,
  * weight        device bf16 [C] or NULL.
  * shift, scale  device fp32 [B, C], both or neither; gate_res device fp32
  *               [B, C] or NULL (NULL without a branch).
- * cu_seqlens    device int32 [B+1] (must be valid; not re-checked here); with
- *               shift and gate_res both NULL it is not read and may be NULL.
+ * cu_seqlens    device int32 [B+1] (must be valid; not re-checked here; tokens
+ *               at or behind cu_seqlens[B] take the last request's vectors);
+ *               with shift and gate_res both NULL it is not read and may be
+ *               NULL.
  * C             a multiple of 8, at most 16384. 0 <= T <= 2^31 - 513. eps > 0.
  */
 PQK_API int pqk_norm_modulate_i8(const void* x, int64_t x_stride_t, const void* branch, int64_t branch_stride_t,
@@ -516,7 +518,8 @@ PQK_API int pqk_quantize_i8(const void* x, int64_t x_stride_t, int64_t T, int C,
  * w8          device int8 [N, K] (out x in features), rows w8_stride_n bytes
  *             apart (a multiple of 16).
  * w_scale     device fp32 [N], 16-byte aligned.
- * x, gate_res, cu_seqlens, out: as pqk_linear_gated_residual.
+ * x, gate_res, cu_seqlens, out: as pqk_linear_gated_residual (a token at or
+ *             behind cu_seqlens[B] takes the last request's gate).
  * K, N        multiples of 8, >= 8; K <= 131071 (the sums fit in int32 for
  *             codes of -128 too); T, N limits as pqk_linear_gated_residual.
  * Errors as pqk_linear_gated_residual.

@@ -169,10 +169,10 @@ struct Layout {
   static constexpr int kVoteOff = kAbortOff + 4;
   // claimed work-tile indices, a ring of kWorkSlots (-1: no more work)
   static constexpr int kWorkOff = kVoteOff + 16;
-  // the producer's copy counts (K/V stages, Q pairs; kCross: K/V stages, first and second Q tiles), left for the
-  // drain
   // (kCross: the decoded units instead, eight words each)
   static constexpr int kUnitOff = (kWorkOff + 15) / 16 * 16;
+  // the producer's copy counts (K/V stages, Q pairs; kCross: K/V stages, first and second Q tiles), left for the
+  // drain
   static constexpr int kLoadsOff = kCross ? kUnitOff + 32 * kWorkSlots : kWorkOff + 4 * kWorkSlots;
   static constexpr int kBytes = kLoadsOff + (kCross ? 12 : 8);
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024
@@ -511,8 +511,10 @@ __global__ void __launch_bounds__(kSchedThreads)
   __syncthreads();
   auto tiles_of = [&](int r) { return (cs.q_len[r] + tile_tokens - 1) / tile_tokens * head_blocks; };
   auto key_tiles_of = [&](int r) { return (cs.k_len[r] + kBN - 1) / kBN; };
-  const int32_t tiles = exclusive_prefix<kSchedThreads>(B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
-  const int32_t empty = exclusive_prefix<kSchedThreads>(B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
+  const int32_t tiles = exclusive_prefix<kSchedThreads>(
+      B, cs.tile_start, [&](int r) { return cs.k_len[r] > 0 ? tiles_of(r) : 0; });
+  const int32_t empty = exclusive_prefix<kSchedThreads>(
+      B, cs.empty_start, [&](int r) { return cs.k_len[r] > 0 ? 0 : tiles_of(r); });
   int part_tiles = 0;
   if (tiles < kCutUnits) {
     unsigned long long mine = 0;
@@ -1571,8 +1573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (valid_row) {
 #pragma unroll
               for (int c = 0; c < 32; c += 4)
-                part[(c0 + c) / 4] = make_float4(__uint_as_float(ov[c]) * inv_l, __uint_as_float(ov[c + 1]) * inv_l,
-                                                 __uint_as_float(ov[c + 2]) * inv_l, __uint_as_float(ov[c + 3]) * inv_l);
+                part[(c0 + c) / 4] =
+                    make_float4(__uint_as_float(ov[c]) * inv_l, __uint_as_float(ov[c + 1]) * inv_l,
+                                __uint_as_float(ov[c + 2]) * inv_l, __uint_as_float(ov[c + 3]) * inv_l);
             }
           }
           if (valid_row) p.part_lse[prow] = m + __log2f(l);
@@ -1767,9 +1770,9 @@ bool set_schedule_smem_attr() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   if (!done[dev]) {
-    if (cudaFuncSetAttribute(kCross ? reinterpret_cast<const void*>(build_cross_schedule_kernel)
-                                    : reinterpret_cast<const void*>(build_schedule_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedSmem) !=
-        cudaSuccess)
+    const void* kernel = kCross ? reinterpret_cast<const void*>(build_cross_schedule_kernel)
+                                : reinterpret_cast<const void*>(build_schedule_kernel);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedSmem) != cudaSuccess)
       return false;
     done[dev] = 1;
   }

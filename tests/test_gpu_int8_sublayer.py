@@ -157,6 +157,38 @@ def test_captured_sublayer_replays_bitwise_with_new_contents(lens_q, lens_k):
     del g
 
 
+def test_two_graphs_that_share_a_workspace_replay_in_turn():
+    torch = torch_cuda()
+    subs = [Sublayer([700, 5, 300], [64, 0, 1300], seed=9), Sublayer([3, 0, 130], [9, 4, 2000], seed=10)]
+    subs[1].o["ws"] = subs[0].o["ws"]
+    refs, graphs = [], []
+    for s in subs:
+        s.run()
+        torch.cuda.synchronize()
+        refs.append({k: v.clone() for k, v in s.o.items() if k != "ws"})
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for s in subs:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                s.run()
+            graphs.append(g)
+    torch.cuda.current_stream().wait_stream(st)
+    for s in subs:
+        for k, v in s.o.items():
+            v.zero_()
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert pqk.get_device_status() == 0
+    for s, ref in zip(subs, refs):
+        for k, want in ref.items():
+            assert torch.equal(s.o[k], want), k
+    del graphs
+
+
 def test_two_streams_at_once_each_with_its_own_buffers():
     torch = torch_cuda()
     subs = [Sublayer([700, 5, 300], [64, 0, 1300], seed=6), Sublayer([1, 0, 130], [9, 4, 700], seed=7)]
