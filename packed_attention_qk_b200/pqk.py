@@ -9,6 +9,7 @@ built, loading fails with an error.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 
@@ -177,8 +178,8 @@ class _Args:
         raise ValueError(f"{self.fn}: {name} {why}")
 
     def first(self, name: str, t, dtype, ndim: int):
-        """The call's first tensor: its shape, once it is a CUDA tensor of the
-        current device with `ndim` dimensions."""
+        """The call's first tensor: its shape and row stride (see rows), once
+        it is a CUDA tensor of the current device with `ndim` dimensions."""
         if not isinstance(t, self.torch.Tensor):
             self.fail(name, "is not a tensor")
         shape = t.shape
@@ -192,7 +193,7 @@ class _Args:
         if dev != self.torch.cuda.current_device():
             self.fail(name, f"is on {t.device}, not on the current device")
         self.dev = dev
-        return shape
+        return shape, self._row_stride(name, t, shape)
 
     def whole(self, name: str, t, dtype, shape) -> None:
         """t must be `dtype`, of `shape` and contiguous."""
@@ -209,14 +210,17 @@ class _Args:
         dimensions but the first). Returns the row stride; for at most one row,
         whose stride means nothing, its length in whole 16-byte units."""
         try:
-            if t.dtype is dtype and t.shape == shape and t.get_device() == self.dev and shape[0] > 1:
-                strides = t.stride()
-                if strides[-1] == 1 and (len(shape) == 2 or strides[1] == shape[2]):
-                    return strides[0]
+            same = t.dtype is dtype and t.shape == shape and t.get_device() == self.dev
         except AttributeError:
             self.fail(name, "is not a tensor")
-        self._kind(name, t, dtype, shape)
+        if not same:
+            self._kind(name, t, dtype, shape)
+        return self._row_stride(name, t, shape)
+
+    def _row_stride(self, name: str, t, shape) -> int:
         strides = t.stride()
+        if shape[0] > 1 and strides[-1] == 1 and (len(shape) == 2 or strides[1] == shape[2]):
+            return strides[0]
         want = 1
         for d in range(len(shape) - 1, 0, -1):
             if strides[d] != want and shape[d] > 1 and t.numel() > 0:
@@ -579,9 +583,8 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
     [B+1]. Returns (x_out or None, h8 int8 [T, C], h_scale fp32 [T])."""
     a = _Args("norm_modulate_i8")
     bf16, f32 = a.torch.bfloat16, a.torch.float32
-    shape = a.first("x", x, bf16, 2)
+    shape, x_stride = a.first("x", x, bf16, 2)
     T, Cdim = shape
-    x_stride = a.rows("x", x, bf16, shape)
     br_stride = 0 if branch is None else a.rows("branch", branch, bf16, shape)
     xo_stride = 0 if x_out is None else a.rows("x_out", x_out, bf16, shape)
     B = _requests(a, cu_seqlens)
@@ -596,9 +599,9 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
     h8, h8_stride = _rows_i8(a, "h8", h8, T, Cdim, x)
     h_scale = _floats(a, "h_scale", h_scale, T, x)
     _check("pqk_norm_modulate_i8", lib().pqk_norm_modulate_i8(
-        _ptr(x), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, _ptr(h8), h8_stride, _ptr(h_scale),
-        _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim, norm_type, eps,
-        _stream(stream)))
+        x.data_ptr(), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, h8.data_ptr(), h8_stride,
+        h_scale.data_ptr(), _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim,
+        norm_type, eps, _stream(stream)))
     _used_on(a, stream, h8, h_scale)
     return x_out, h8, h_scale
 
@@ -608,22 +611,18 @@ def quantize_i8(x, *, x8=None, scales=None, stream=None):
     (max |x| / 127). Returns (x8 int8 [T, C], scales fp32 [T])."""
     a = _Args("quantize_i8")
     bf16 = a.torch.bfloat16
-    shape = a.first("x", x, bf16, 2)
-    T, Cdim = shape
-    x_stride = a.rows("x", x, bf16, shape)
+    (T, Cdim), x_stride = a.first("x", x, bf16, 2)
     x8, x8_stride = _rows_i8(a, "x8", x8, T, Cdim, x)
     scales = _floats(a, "scales", scales, T, x)
-    _check("pqk_quantize_i8", lib().pqk_quantize_i8(_ptr(x), x_stride, T, Cdim, _ptr(x8), x8_stride, _ptr(scales),
-                                                     _stream(stream)))
+    _check("pqk_quantize_i8", lib().pqk_quantize_i8(x.data_ptr(), x_stride, T, Cdim, x8.data_ptr(), x8_stride,
+                                                    scales.data_ptr(), _stream(stream)))
     _used_on(a, stream, x8, scales)
     return x8, scales
 
 
 def _i8_operands(a: _Args, a8, a_scale, w8, w_scale):
     i8, f32 = a.torch.int8, a.torch.float32
-    shape = a.first("a8", a8, i8, 2)
-    T, K = shape
-    a_stride = a.rows("a8", a8, i8, shape)
+    (T, K), a_stride = a.first("a8", a8, i8, 2)
     if not isinstance(w8, a.torch.Tensor) or w8.dim() != 2:
         a.fail("w8", "is not a two-dimensional tensor")
     N = w8.shape[0]
@@ -648,8 +647,8 @@ def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None,
         a.whole("gate_res", gate_res, a.torch.float32, (B, N))
     out, out_stride = _rows_bf16(a, "out", out, (T, N), a8)
     _check("pqk_linear_i8_gated_residual", lib().pqk_linear_i8_gated_residual(
-        _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(x), x_stride, _ptr(gate_res),
-        _ptr(cu_seqlens), B, _ptr(out), out_stride, T, K, N, _stream(stream)))
+        a8.data_ptr(), a_stride, a_scale.data_ptr(), w8.data_ptr(), w_stride, w_scale.data_ptr(), _ptr(x), x_stride,
+        _ptr(gate_res), _ptr(cu_seqlens), B, out.data_ptr(), out_stride, T, K, N, _stream(stream)))
     _used_on(a, stream, out)
     return out
 
@@ -665,12 +664,13 @@ def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
         a.fail("w8", "has an odd number of rows")
     act, act_stride = _rows_bf16(a, "act", act, (T, F), a8)
     _check("pqk_linear_i8_swiglu", lib().pqk_linear_i8_swiglu(
-        _ptr(a8), a_stride, _ptr(a_scale), _ptr(w8), w_stride, _ptr(w_scale), _ptr(act), act_stride, T, K, F,
-        _stream(stream)))
+        a8.data_ptr(), a_stride, a_scale.data_ptr(), w8.data_ptr(), w_stride, w_scale.data_ptr(), act.data_ptr(),
+        act_stride, T, K, F, _stream(stream)))
     _used_on(a, stream, act)
     return act
 
 
+@functools.lru_cache(maxsize=64)
 def varlen_cross_attn_workspace_size(B: int, D: int) -> int:
     return int(lib().pqk_varlen_cross_attn_workspace_size(B, D))
 
@@ -685,14 +685,14 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     fp32 [H, Tq] or None)."""
     a = _Args("varlen_cross_attn_fwd")
     torch, bf16 = a.torch, a.torch.bfloat16
-    shape = a.first("q", q, bf16, 3)
+    shape, q_stride = a.first("q", q, bf16, 3)
     Tq, H, D = shape
-    q_stride = a.rows("q", q, bf16, shape)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         a.fail("k", "is not a three-dimensional tensor")
     Tk, Hkv = k.shape[:2]
-    k_stride = a.rows("k", k, bf16, (Tk, Hkv, D))
-    v_stride = a.rows("v", v, bf16, (Tk, Hkv, D))
+    kv_shape = (Tk, Hkv, D)
+    k_stride = a.rows("k", k, bf16, kv_shape)
+    v_stride = a.rows("v", v, bf16, kv_shape)
     if cu_seqlens_q is None:
         a.fail("cu_seqlens_q", "is not a one-dimensional tensor")
     B = _requests(a, cu_seqlens_q, "cu_seqlens_q")
@@ -708,9 +708,9 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != q.device:
         a.fail("workspace", f"is not a contiguous tensor on {q.device}")
     _check("pqk_varlen_cross_attn_fwd", lib().pqk_varlen_cross_attn_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), q_stride, k_stride, v_stride, o_stride, _ptr(cu_seqlens_q),
-        _ptr(cu_seqlens_k), B, Tq, Tk, H, Hkv, D, scale, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), q_stride, k_stride, v_stride, o_stride,
+        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq, Tk, H, Hkv, D, scale, workspace.data_ptr(),
+        workspace.nbytes, _stream(stream)))
     _used_on(a, stream, o, lse, workspace)
     return o, lse
 
