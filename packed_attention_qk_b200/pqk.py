@@ -169,10 +169,10 @@ class _Args:
     usually gets, a contiguous tensor of the right shape, passes in one
     comparison: the checks of a call cost about as much as its launch."""
 
-    __slots__ = ("fn", "torch", "dev")
+    __slots__ = ("fn", "torch", "dev", "device")
 
     def __init__(self, fn: str):
-        self.fn, self.torch, self.dev = fn, _torch or _load_torch(), None
+        self.fn, self.torch, self.dev, self.device = fn, _torch or _load_torch(), None, None
 
     def fail(self, name: str, why: str):
         raise ValueError(f"{self.fn}: {name} {why}")
@@ -190,9 +190,9 @@ class _Args:
         dev = t.get_device()
         if dev < 0:
             self.fail(name, f"is on {t.device}, not on a CUDA device")
-        if dev != self.torch.cuda.current_device():
+        if dev != self.torch._C._cuda_getDevice():
             self.fail(name, f"is on {t.device}, not on the current device")
-        self.dev = dev
+        self.dev, self.device = dev, t.device
         return shape, self._row_stride(name, t, shape)
 
     def whole(self, name: str, t, dtype, shape) -> None:
@@ -242,6 +242,24 @@ class _Args:
             self.fail(name, f"is on {t.device}, not on cuda:{self.dev}")
 
 
+    def new(self, dtype, *shape):
+        """A new contiguous tensor on the call's device (with the strides given
+        an allocation takes 1.5 us instead of 2.0)."""
+        if len(shape) == 1:
+            strides = (1,)
+        elif len(shape) == 2:
+            strides = (shape[1], 1)
+        else:
+            strides = (shape[1] * shape[2], shape[2], 1)
+        return self.torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+
+    def stream(self, stream) -> int:
+        """The handle of the caller's stream, or the current one's."""
+        if stream is None:
+            return self.torch._C._cuda_getCurrentRawStream(self.dev)
+        return _stream(stream)
+
+
 def _used_on(a: _Args, stream, *tensors) -> None:
     """Tensors that a call allocated (on the current stream's account) and used
     on a stream of the caller's choice: their memory is not handed out again
@@ -264,29 +282,29 @@ def _requests(a: _Args, cu_seqlens, name: str = "cu_seqlens") -> int:
     return n - 1
 
 
-def _rows_i8(a: _Args, name: str, t, T: int, C: int, like):
-    """The int8 [T, C] tensor t, or a new one on like's device whose rows start
-    on 16-byte boundaries, and its row stride."""
+def _rows_i8(a: _Args, name: str, t, T: int, C: int):
+    """The int8 [T, C] tensor t, or a new one whose rows start on 16-byte
+    boundaries, and its row stride."""
     if t is not None:
         return t, a.rows(name, t, a.torch.int8, (T, C))
     wide = (C + 15) // 16 * 16
-    t = like.new_empty((T, wide), dtype=a.torch.int8)
+    t = a.new(a.torch.int8, T, wide)
     return (t if wide == C else t[:, :C]), wide
 
 
-def _floats(a: _Args, name: str, t, n: int, like):
+def _floats(a: _Args, name: str, t, n: int):
     """The fp32 [n] tensor t, or a new one."""
     if t is None:
-        return like.new_empty(n, dtype=a.torch.float32)
+        return a.new(a.torch.float32, n)
     a.whole(name, t, a.torch.float32, (n,))
     return t
 
 
-def _rows_bf16(a: _Args, name: str, t, shape, like):
+def _rows_bf16(a: _Args, name: str, t, shape):
     """The bf16 tensor t of `shape`, or a new one, and its row stride."""
     if t is not None:
         return t, a.rows(name, t, a.torch.bfloat16, shape)
-    t = like.new_empty(shape, dtype=a.torch.bfloat16)
+    t = a.new(a.torch.bfloat16, *shape)
     return t, math.prod(shape[1:])
 
 
@@ -596,12 +614,12 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
         a.whole("scale", scale, f32, (B, Cdim))
     if weight is not None:
         a.whole("weight", weight, bf16, (Cdim,))
-    h8, h8_stride = _rows_i8(a, "h8", h8, T, Cdim, x)
-    h_scale = _floats(a, "h_scale", h_scale, T, x)
+    h8, h8_stride = _rows_i8(a, "h8", h8, T, Cdim)
+    h_scale = _floats(a, "h_scale", h_scale, T)
     _check("pqk_norm_modulate_i8", lib().pqk_norm_modulate_i8(
         x.data_ptr(), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, h8.data_ptr(), h8_stride,
         h_scale.data_ptr(), _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim,
-        norm_type, eps, _stream(stream)))
+        norm_type, eps, a.stream(stream)))
     _used_on(a, stream, h8, h_scale)
     return x_out, h8, h_scale
 
@@ -612,10 +630,10 @@ def quantize_i8(x, *, x8=None, scales=None, stream=None):
     a = _Args("quantize_i8")
     bf16 = a.torch.bfloat16
     (T, Cdim), x_stride = a.first("x", x, bf16, 2)
-    x8, x8_stride = _rows_i8(a, "x8", x8, T, Cdim, x)
-    scales = _floats(a, "scales", scales, T, x)
+    x8, x8_stride = _rows_i8(a, "x8", x8, T, Cdim)
+    scales = _floats(a, "scales", scales, T)
     _check("pqk_quantize_i8", lib().pqk_quantize_i8(x.data_ptr(), x_stride, T, Cdim, x8.data_ptr(), x8_stride,
-                                                    scales.data_ptr(), _stream(stream)))
+                                                    scales.data_ptr(), a.stream(stream)))
     _used_on(a, stream, x8, scales)
     return x8, scales
 
@@ -645,10 +663,10 @@ def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None,
     x_stride = 0 if x is None else a.rows("x", x, a.torch.bfloat16, (T, N))
     if gate_res is not None:
         a.whole("gate_res", gate_res, a.torch.float32, (B, N))
-    out, out_stride = _rows_bf16(a, "out", out, (T, N), a8)
+    out, out_stride = _rows_bf16(a, "out", out, (T, N))
     _check("pqk_linear_i8_gated_residual", lib().pqk_linear_i8_gated_residual(
         a8.data_ptr(), a_stride, a_scale.data_ptr(), w8.data_ptr(), w_stride, w_scale.data_ptr(), _ptr(x), x_stride,
-        _ptr(gate_res), _ptr(cu_seqlens), B, out.data_ptr(), out_stride, T, K, N, _stream(stream)))
+        _ptr(gate_res), _ptr(cu_seqlens), B, out.data_ptr(), out_stride, T, K, N, a.stream(stream)))
     _used_on(a, stream, out)
     return out
 
@@ -662,10 +680,10 @@ def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
     F, odd = divmod(rows, 2)
     if odd:
         a.fail("w8", "has an odd number of rows")
-    act, act_stride = _rows_bf16(a, "act", act, (T, F), a8)
+    act, act_stride = _rows_bf16(a, "act", act, (T, F))
     _check("pqk_linear_i8_swiglu", lib().pqk_linear_i8_swiglu(
         a8.data_ptr(), a_stride, a_scale.data_ptr(), w8.data_ptr(), w_stride, w_scale.data_ptr(), act.data_ptr(),
-        act_stride, T, K, F, _stream(stream)))
+        act_stride, T, K, F, a.stream(stream)))
     _used_on(a, stream, act)
     return act
 
@@ -698,19 +716,19 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     B = _requests(a, cu_seqlens_q, "cu_seqlens_q")
     a.whole("cu_seqlens_k", cu_seqlens_k, torch.int32, (B + 1,))
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
-    o, o_stride = _rows_bf16(a, "o", o, shape, q)
+    o, o_stride = _rows_bf16(a, "o", o, shape)
     if lse is not None:
         a.whole("lse", lse, torch.float32, (H, Tq))
     elif want_lse:
-        lse = q.new_empty((H, Tq), dtype=torch.float32)
+        lse = a.new(torch.float32, H, Tq)
     if workspace is None:
-        workspace = q.new_empty(varlen_cross_attn_workspace_size(B, D), dtype=torch.uint8)
-    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != q.device:
-        a.fail("workspace", f"is not a contiguous tensor on {q.device}")
+        workspace = a.new(torch.uint8, varlen_cross_attn_workspace_size(B, D))
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != a.device:
+        a.fail("workspace", f"is not a contiguous tensor on {a.device}")
     _check("pqk_varlen_cross_attn_fwd", lib().pqk_varlen_cross_attn_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), q_stride, k_stride, v_stride, o_stride,
         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq, Tk, H, Hkv, D, scale, workspace.data_ptr(),
-        workspace.nbytes, _stream(stream)))
+        workspace.nbytes, a.stream(stream)))
     _used_on(a, stream, o, lse, workspace)
     return o, lse
 
