@@ -459,9 +459,12 @@ PQK_API int pqk_linear_swiglu(const void* a, int64_t a_stride_t, const void* w1,
  *   h    = norm(x') * weight * (1 + scale[s]) + shift[s]  (pqk_norm_type over
  *          C; weight NULL: 1; scale and shift NULL: norm(x') * weight)
  *   h_scale[t] = max_c |h_c| / 127, or 1 when every h_c is 0
- *   h8[t, c]   = h_c / h_scale[t] rounded to the nearest integer, ties to
- *                even, so in -127..127
- * fp32 arithmetic; h is not rounded before it is coded. A token with an
+ *   h8[t, c]   = 127 h_c / max_c |h_c| rounded to the nearest integer, ties to
+ *                even, so in -127..127 (h_c / h_scale[t] before h_scale[t] is
+ *                rounded to fp32)
+ * fp32 arithmetic; h is not rounded before it is coded, and the quotient is
+ * rounded to fp32 once, so that ties are kept: the codes of bf16 rows are
+ * exactly these. A token with an
  * infinite or NaN h_c (or whose mean square passes fp32's range) gets h_scale
  * NaN and codes 0: its dequantised row is NaN, the other tokens' are not
  * affected.

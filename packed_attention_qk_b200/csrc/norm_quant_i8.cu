@@ -7,11 +7,13 @@
 //
 //   x' = x + gate_res[s] * branch          (either may be left out)
 //   h  = norm(x') * weight * (1 + scale[s]) + shift[s]
-//   step = max_c |h_c| / 127 (1 for a zero row), code_c = rint(h_c / step)
+//   step = max_c |h_c| / 127 (1 for a zero row)
+//   code_c = 127 h_c / max_c |h_c| to the nearest integer, ties to even
 //
 // HBM-bound: x and branch are read once, x' and the codes written once (7
 // bytes an element with everything on). kTpr threads own one row and hold all
-// of it in registers as fp32, kCpt chunks of 8 elements a thread, so the three
+// of it in registers as fp32 (as bf16 where x itself is coded), kCpt chunks of 8
+// elements a thread, so the three
 // dependent passes over a row (its moments, its largest |h|, its codes) cost
 // no memory traffic and h is never rounded before it is coded. Rows of one
 // warp need only shuffles; longer ones exchange one word per warp.
@@ -59,6 +61,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     f[2 * i] = __uint_as_float(w[i] << 16);
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+}
+
+// Bits of the largest of eight |bf16|, as an fp32 number.
+__device__ __forceinline__ uint32_t max_abs_bf16x8(const uint4& v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+  return max(m << 16, m & 0xffff0000u);
 }
 
 __device__ __forceinline__ uint4 ld16(const void* p) {
@@ -126,14 +135,14 @@ struct MaxOp {
 // Threads per block: one row, or four of a warp each (blocks of two or four
 // rows of 128 threads leave more of an SM idle between rows: 364 and 491 us
 // where these take 348 for [58,048, 5,120]). And the blocks per SM that the
-// registers have to allow where the compiler would use more: 80 registers with
-// 7 chunks of x alone (12,345 rows of 13,824: 127 -> 104 us), 72 with 5 chunks
-// of everything (58,048 rows of 5,120: 357 -> 348 us, without the branch 250 ->
-// 233).
+// registers have to allow where the compiler would use more: 40 registers for
+// 512 threads on x alone (12,345 rows of 16,384: 118 -> 105 us, of 14,344: 113 ->
+// 98), 72 with 5 chunks of everything (58,048 rows of 5,120: 357 -> 348 us,
+// without the branch 250 -> 233).
 template <int kTpr>
 constexpr int kBlock = kTpr < 128 ? 128 : kTpr;
 template <int kTpr, int kCpt, bool kPlain>
-constexpr int kBlocksPerSm = kPlain && kTpr == 256 && kCpt >= 6 ? 3 : (!kPlain && kTpr == 128 && kCpt == 5 ? 7 : 1);
+constexpr int kBlocksPerSm = kPlain && kTpr == 512 ? 3 : (!kPlain && kTpr == 128 && kCpt == 5 ? 7 : 1);
 
 // kPlain: codes of x alone (no branch, norm or vectors), in fewer registers.
 template <int kTpr, int kCpt, bool kPlain>
@@ -152,15 +161,17 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
   const int64_t mod_row =
       !kPlain && p.cu != nullptr ? static_cast<int64_t>(find_segment(p.cu, p.B, t)) * p.C : 0;
 
-  float v[kCpt][8];
-  {
-    uint4 xr[kCpt], br[kCpt];
+  uint4 xr[kCpt];
 #pragma unroll
-    for (int i = 0; i < kCpt; ++i) {
-      const int c = lane + i * kTpr;
-      xr[i] = c < nchunks ? ld16(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
-    }
-    if (!kPlain && p.branch != nullptr) {
+  for (int i = 0; i < kCpt; ++i) {
+    const int c = lane + i * kTpr;
+    xr[i] = c < nchunks ? ld16(p.x + t * p.x_stride + c * 8) : make_uint4(0, 0, 0, 0);
+  }
+  // the row in fp32; codes of x alone keep it as it came, in half the registers
+  float v[kPlain ? 1 : kCpt][8];
+  if constexpr (!kPlain) {
+    uint4 br[kCpt];
+    if (p.branch != nullptr) {
 #pragma unroll
       for (int i = 0; i < kCpt; ++i) {
         const int c = lane + i * kTpr;
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
     for (int i = 0; i < kCpt; ++i) {
       const int c = lane + i * kTpr;
       unpack8(xr[i], v[i]);
-      if (!kPlain && p.branch != nullptr && c < nchunks) {
+      if (p.branch != nullptr && c < nchunks) {
         float b[8], g[8];
         unpack8(br[i], b);
         if (p.gate_res != nullptr) {
@@ -187,91 +198,125 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
   }
   // x' of every element is formed by the thread that read the element: x_out
   // may be x (or branch) itself
-  if (!kPlain && p.x_out != nullptr) {
+  if constexpr (!kPlain) {
+    if (p.x_out != nullptr) {
 #pragma unroll
-    for (int i = 0; i < kCpt; ++i) {
-      const int c = lane + i * kTpr;
-      if (c < nchunks) {
-        uint4 o;
-        o.x = pack_bf16x2(v[i][0], v[i][1]);
-        o.y = pack_bf16x2(v[i][2], v[i][3]);
-        o.z = pack_bf16x2(v[i][4], v[i][5]);
-        o.w = pack_bf16x2(v[i][6], v[i][7]);
-        *reinterpret_cast<uint4*>(p.x_out + t * p.x_out_stride + c * 8) = o;
-      }
-    }
-  }
-
-  const float inv_c = 1.0f / static_cast<float>(p.C);
-  if (!kPlain && p.norm_type != 2) {
-    float mu = 0.f;
-    if (p.norm_type == 1) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < kCpt; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[i][e];
-      mu = row_reduce<kTpr>(s, s_sum[group][0], AddOp()) * inv_c;
-    }
-    // centred second moment (mu = 0 for RMS); elements past C stay 0
-    float s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < kCpt; ++i) {
-      if (lane + i * kTpr < nchunks) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[i][e] -= mu;
-          s2 = fmaf(v[i][e], v[i][e], s2);
+      for (int i = 0; i < kCpt; ++i) {
+        const int c = lane + i * kTpr;
+        if (c < nchunks) {
+          uint4 o;
+          o.x = pack_bf16x2(v[i][0], v[i][1]);
+          o.y = pack_bf16x2(v[i][2], v[i][3]);
+          o.z = pack_bf16x2(v[i][4], v[i][5]);
+          o.w = pack_bf16x2(v[i][6], v[i][7]);
+          *reinterpret_cast<uint4*>(p.x_out + t * p.x_out_stride + c * 8) = o;
         }
       }
     }
-    s2 = row_reduce<kTpr>(s2, s_sum[group][1], AddOp()) * inv_c;
-    // squares past fp32's range: the row counts as not finite
-    const float inv = s2 <= 3.402823466e38f ? 1.0f / sqrtf(s2 + p.eps) : __int_as_float(0x7fffffff);
+
+    const float inv_c = 1.0f / static_cast<float>(p.C);
+    if (p.norm_type != 2) {
+      float mu = 0.f;
+      if (p.norm_type == 1) {
+        float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kCpt; ++i)
+        for (int i = 0; i < kCpt; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= inv;
+          for (int e = 0; e < 8; ++e) s += v[i][e];
+        mu = row_reduce<kTpr>(s, s_sum[group][0], AddOp()) * inv_c;
+      }
+      // centred second moment (mu = 0 for RMS); elements past C stay 0
+      float s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCpt; ++i) {
+        if (lane + i * kTpr < nchunks) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[i][e] -= mu;
+            s2 = fmaf(v[i][e], v[i][e], s2);
+          }
+        }
+      }
+      s2 = row_reduce<kTpr>(s2, s_sum[group][1], AddOp()) * inv_c;
+      // squares past fp32's range: the row counts as not finite
+      const float inv = s2 <= 3.402823466e38f ? 1.0f / sqrtf(s2 + p.eps) : __int_as_float(0x7fffffff);
+#pragma unroll
+      for (int i = 0; i < kCpt; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= inv;
+    }
   }
   uint32_t top = 0;  // bits of the largest |h|
 #pragma unroll
   for (int i = 0; i < kCpt; ++i) {
     const int c = lane + i * kTpr;
     if (c < nchunks) {
-      if (!kPlain && p.weight != nullptr) {
-        float w[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight + c * 8)), w);
+      if constexpr (kPlain) {
+        top = max(top, max_abs_bf16x8(xr[i]));
+      } else {
+        if (p.weight != nullptr) {
+          float w[8];
+          unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight + c * 8)), w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
+          for (int e = 0; e < 8; ++e) v[i][e] *= w[e];
+        }
+        if (p.shift != nullptr) {
+          float sc[8], sh[8];
+          load8f(p.scale + mod_row + c * 8, p.wide, sc);
+          load8f(p.shift + mod_row + c * 8, p.wide, sh);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] = fmaf(v[i][e], 1.0f + sc[e], sh[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
       }
-      if (!kPlain && p.shift != nullptr) {
-        float sc[8], sh[8];
-        load8f(p.scale + mod_row + c * 8, p.wide, sc);
-        load8f(p.shift + mod_row + c * 8, p.wide, sh);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = fmaf(v[i][e], 1.0f + sc[e], sh[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
     }
   }
   top = row_reduce<kTpr>(top, s_max[group], MaxOp());
 
   const bool finite = top < 0x7f800000u;
   const float amax = __uint_as_float(top);
-  // 127 / amax overflows below 2^-121: such rows are coded from h * 2^64
-  const float up = amax < 7.888609052e-31f ? 18446744073709551616.0f : 1.0f;
-  const float to_code = amax > 0.f ? 127.0f / (amax * up) : 0.f;
+  // 127 / amax as hi + lo, whose sum is off by less than 2^-46 of it: the
+  // quotient below is the real one rounded once (but for real ones within 2^-40
+  // of the border between two floats), and a tie stays a tie. With hi alone an
+  // element of half the row's maximum, 63.5 steps, was coded 63 for 66 of the 128
+  // mantissas that a bf16 maximum can have. Rows whose hi or lo would overflow or
+  // be subnormal are scaled by a power of two first.
+  const float shift_by = amax < 7.888609052e-31f  ? 18446744073709551616.0f  // 2^-100, 2^64
+                         : amax > 1.267650600e30f ? 5.421010862e-20f         // 2^100, 2^-64
+                                                  : 1.0f;
+  const float a = amax * shift_by;
+  if constexpr (!kPlain) {
+    if (shift_by != 1.0f) {
+#pragma unroll
+      for (int i = 0; i < kCpt; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= shift_by;
+    }
+  }
+  const float hi = a > 0.f ? 127.0f / a : 0.f;
+  const float lo = fmaf(-hi, a, 127.0f) * (hi * (1.0f / 127.0f));
   if (lane == 0) p.h_scale[t] = finite ? (amax > 0.f ? amax / 127.0f : 1.0f) : __int_as_float(0x7fffffff);
 #pragma unroll
   for (int i = 0; i < kCpt; ++i) {
     const int c = lane + i * kTpr;
     if (c < nchunks) {
-      // h * to_code + 1.5 * 2^23: the integer nearest to the product (ties to
-      // even, no rounding in between) is the sum's low byte
+      float h[8];
+      if constexpr (kPlain) {
+        unpack8(xr[i], h);
+        if (shift_by != 1.0f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] *= shift_by;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = v[i][e];
+      }
+      // the quotient + 1.5 * 2^23: the integer nearest to it (ties to even) is
+      // the sum's low byte
       uint32_t q[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(fmaf(v[i][e] * up, to_code, 12582912.0f));
+      for (int e = 0; e < 8; ++e) q[e] = __float_as_uint(fmaf(h[e], hi, h[e] * lo) + 12582912.0f);
       uint2 o;
       o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
       o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
