@@ -223,7 +223,9 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
         for (int i = 0; i < kCpt; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e) s += v[i][e];
-        mu = row_reduce<kTpr>(s, s_sum[group][0], AddOp()) * inv_c;
+        // a quotient, not a product with 1 / C: a constant row's sum is exact, and
+        // its mean has to be that constant
+        mu = row_reduce<kTpr>(s, s_sum[group][0], AddOp()) / static_cast<float>(p.C);
       }
       // centred second moment (mu = 0 for RMS); elements past C stay 0
       float s2 = 0.f;
