@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
   constexpr int kRows = kBlock<kTpr> / kTpr;
   // one set of words for each of a row's exchanges, so that no exchange can
   // overwrite words that a slow warp still reads
-  __shared__ float s_sum[kRows][2][kTpr / 32];
+  __shared__ float s_sum[kRows][3][kTpr / 32];
   __shared__ uint32_t s_max[kRows][kTpr / 32];
   const int group = threadIdx.x / kTpr;
   const int lane = threadIdx.x % kTpr;
@@ -239,9 +239,26 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
           }
         }
       }
-      s2 = row_reduce<kTpr>(s2, s_sum[group][1], AddOp()) * inv_c;
-      // squares past fp32's range: the row counts as not finite
-      const float inv = s2 <= 3.402823466e38f ? 1.0f / sqrtf(s2 + p.eps) : __int_as_float(0x7fffffff);
+      s2 = row_reduce<kTpr>(s2, s_sum[group][1], AddOp());
+      float inv;
+      if (s2 <= 3.402823466e38f) {
+        inv = 1.0f / sqrtf(s2 * inv_c + p.eps);
+      } else {
+        // The sum passed fp32's range; the mean square need not have: sum the
+        // squares of 2^-12 v (C is at most 2^14). A row whose mean square passes
+        // it counts as not finite.
+        float small = 0.f;
+#pragma unroll
+        for (int i = 0; i < kCpt; ++i) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float u = lane + i * kTpr < nchunks ? v[i][e] * 0x1p-12f : 0.f;
+            small = fmaf(u, u, small);
+          }
+        }
+        const float mean = row_reduce<kTpr>(small, s_sum[group][2], AddOp()) * inv_c * 0x1p24f;
+        inv = mean <= 3.402823466e38f ? 1.0f / sqrtf(mean + p.eps) : __int_as_float(0x7fffffff);
+      }
 #pragma unroll
       for (int i = 0; i < kCpt; ++i)
 #pragma unroll

@@ -37,3 +37,41 @@ def test_constant_rows_have_no_variance(C, repeat):
     assert (s == 1.0).all() and not c.any()
     assert (s2 == 1.0).all() and not c2.any()
     assert (s3 == torch.tensor(2.0) / 127).all() and (c3 == -127).all()
+
+
+@pytest.mark.parametrize("C", [256, 1504, 5120, 16384])
+@pytest.mark.parametrize("norm", [pqk.NORM_RMS, pqk.NORM_LAYER])
+@pytest.mark.parametrize("T", [3, 320])
+def test_mean_squares_up_to_the_end_of_the_range(C, norm, T):
+    """A row's mean square may be anywhere in fp32's range, whatever the sum of its C squares is; past it the row is
+    marked. Neighbours of either kind are not touched. The bound is that of rows of ordinary size: their rounding
+    errors do not depend on the power of two in front."""
+    torch = torch_cuda()
+    g = np.random.default_rng(C + norm + T)
+    x = g.standard_normal((T, C))
+    x[:, 0] += 0.5
+    plain = x.copy()
+    big = np.arange(T) % 3 == 0                                       # mean squares near 2^126.7: sums past the range
+    past = np.arange(T) % 3 == 1                                      # and near 2^130
+    x[big] *= 2.0 ** 63.35
+    x[past] *= 2.0 ** 65
+    w = _bits(g.uniform(0.5, 1.5, C))
+    bits = _bits(x)
+    _, c, s = pqk.norm_modulate_i8(to_dev_bf16(bits), weight=to_dev_bf16(w), norm_type=norm)
+    torch.cuda.synchronize()
+    c, s = c.cpu().numpy(), s.cpu().numpy().astype(np.float64)
+    xd = wl.bf16_bits_to_f64(bits)
+    h = xd - (xd.mean(1, keepdims=True) if norm == pqk.NORM_LAYER else 0)
+    ms = (h * h).mean(1, keepdims=True)
+    top = float(np.finfo(np.float32).max)
+    assert (ms[big] < 0.95 * top).all() and (C * ms[big] > 2 * top).all() and (ms[past] > 1.5 * top).all()
+    h = h / np.sqrt(ms + 1e-6) * wl.bf16_bits_to_f64(w)
+    assert np.isnan(s[past]).all() and not c[past].any()
+    keep = ~past
+    ref = np.abs(h[keep]).max(axis=1) / 127
+    assert (np.abs(s[keep] - ref) <= 128 * 2.0 ** -24 * 2 * ref).all()
+    assert (np.abs(c[keep] - h[keep] / ref[:, None]) <= 0.5 + 127 * 256 * 2.0 ** -24).all()
+    _, c0, s0 = pqk.norm_modulate_i8(to_dev_bf16(_bits(plain)), weight=to_dev_bf16(w), norm_type=norm)
+    rest = ~(big | past)
+    assert np.array_equal(c[rest], c0.cpu().numpy()[rest])
+    assert np.array_equal(s[rest], s0.cpu().numpy().astype(np.float64)[rest])
