@@ -2,7 +2,10 @@
 
 Argument marshalling only: every step of the hot path runs in the CUDA
 kernels behind the C ABI. PyTorch supplies device memory (``data_ptr``) and
-the current CUDA stream. There is no fallback: if ``libpqk.so`` has not been
+the current CUDA stream, or the caller's choice of one (``stream``: a torch
+stream or a raw handle). Ordering such a call behind the work that makes its
+inputs, and the readers of its outputs behind it, is the caller's part, as with
+torch's own operations. There is no fallback: if ``libpqk.so`` has not been
 built, loading fails with an error.
 """
 
@@ -163,16 +166,30 @@ def _load_torch():
     return torch
 
 
+def _stream_object(stream):
+    """The torch stream of a call's `stream`: None, a stream or a raw handle."""
+    if not isinstance(stream, int):
+        return stream
+    cuda = (_torch or _load_torch()).cuda
+    # ExternalStream(0) is a new stream, not the default one
+    return cuda.ExternalStream(stream) if stream != 0 else cuda.default_stream()
+
+
 class _Args:
     """Checks of one call's tensors: type, shape, unit stride inside a row,
     and the current CUDA device (the library launches on it). What a call
     usually gets, a contiguous tensor of the right shape, passes in one
-    comparison: the checks of a call cost about as much as its launch."""
+    comparison: the checks of a call cost about as much as its launch.
 
-    __slots__ = ("fn", "torch", "dev", "device")
+    What the call allocates belongs to the stream that it runs on: memory
+    that the current stream freed may still be read or written by work queued
+    there, and a call on another stream is not ordered behind that work."""
 
-    def __init__(self, fn: str):
+    __slots__ = ("fn", "torch", "dev", "device", "side")
+
+    def __init__(self, fn: str, stream=None):
         self.fn, self.torch, self.dev, self.device = fn, _torch or _load_torch(), None, None
+        self.side = _stream_object(stream)
 
     def fail(self, name: str, why: str):
         raise ValueError(f"{self.fn}: {name} {why}")
@@ -241,34 +258,37 @@ class _Args:
         if t.get_device() != self.dev:
             self.fail(name, f"is on {t.device}, not on cuda:{self.dev}")
 
-
     def new(self, dtype, *shape):
         """A new contiguous tensor on the call's device (with the strides given
-        an allocation takes 1.5 us instead of 2.0)."""
+        an allocation takes 1.5 us instead of 2.0), for the call's stream to
+        write and the caller's current stream to read."""
         if len(shape) == 1:
             strides = (1,)
         elif len(shape) == 2:
             strides = (shape[1], 1)
         else:
             strides = (shape[1] * shape[2], shape[2], 1)
-        return self.torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+        if self.side is None:
+            return self.torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+        with self.torch.cuda.stream(self.side):
+            t = self.torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
+        t.record_stream(self.torch.cuda.current_stream())
+        return t
 
-    def stream(self, stream) -> int:
+    def stream(self) -> int:
         """The handle of the caller's stream, or the current one's."""
-        if stream is None:
+        if self.side is None:
             return self.torch._C._cuda_getCurrentRawStream(self.dev)
-        return _stream(stream)
+        return self.side.cuda_stream
 
-
-def _used_on(a: _Args, stream, *tensors) -> None:
-    """Tensors that a call allocated (on the current stream's account) and used
-    on a stream of the caller's choice: their memory is not handed out again
-    before that stream is through with it."""
-    if stream is not None:
-        s = a.torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
+    def used(self, *tensors) -> None:
+        """The caller's own outputs and workspace, written on a stream of its
+        choice: their memory is not handed out again before that stream is
+        through with it."""
+        if self.side is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.side)
 
 
 def _requests(a: _Args, cu_seqlens, name: str = "cu_seqlens") -> int:
@@ -599,7 +619,7 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
     x, branch, x_out: bf16 [T, C] (rows may be strided; x_out may be x);
     weight bf16 [C]; gate_res, shift, scale fp32 [B, C]; cu_seqlens int32
     [B+1]. Returns (x_out or None, h8 int8 [T, C], h_scale fp32 [T])."""
-    a = _Args("norm_modulate_i8")
+    a = _Args("norm_modulate_i8", stream)
     bf16, f32 = a.torch.bfloat16, a.torch.float32
     shape, x_stride = a.first("x", x, bf16, 2)
     T, Cdim = shape
@@ -619,22 +639,22 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
     _check("pqk_norm_modulate_i8", lib().pqk_norm_modulate_i8(
         x.data_ptr(), x_stride, _ptr(branch), br_stride, _ptr(x_out), xo_stride, h8.data_ptr(), h8_stride,
         h_scale.data_ptr(), _ptr(weight), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens), B, T, Cdim,
-        norm_type, eps, a.stream(stream)))
-    _used_on(a, stream, h8, h_scale)
+        norm_type, eps, a.stream()))
+    a.used(x_out, h8, h_scale)
     return x_out, h8, h_scale
 
 
 def quantize_i8(x, *, x8=None, scales=None, stream=None):
     """The rows of a bf16 tensor [T, C] as int8 codes with one scale per row
     (max |x| / 127). Returns (x8 int8 [T, C], scales fp32 [T])."""
-    a = _Args("quantize_i8")
+    a = _Args("quantize_i8", stream)
     bf16 = a.torch.bfloat16
     (T, Cdim), x_stride = a.first("x", x, bf16, 2)
     x8, x8_stride = _rows_i8(a, "x8", x8, T, Cdim)
     scales = _floats(a, "scales", scales, T)
     _check("pqk_quantize_i8", lib().pqk_quantize_i8(x.data_ptr(), x_stride, T, Cdim, x8.data_ptr(), x8_stride,
-                                                    scales.data_ptr(), a.stream(stream)))
-    _used_on(a, stream, x8, scales)
+                                                    scales.data_ptr(), a.stream()))
+    a.used(x8, scales)
     return x8, scales
 
 
@@ -657,7 +677,7 @@ def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None,
     [T, K], w8: int8 [N, K] (rows on 16-byte boundaries, as quantize_i8 and
     norm_modulate_i8 give them), a_scale fp32 [T], w_scale fp32 [N], x bf16
     [T, N], gate_res fp32 [B, N]. out (bf16) may be x (in place)."""
-    a = _Args("linear_i8_gated_residual")
+    a = _Args("linear_i8_gated_residual", stream)
     T, K, N, a_stride, w_stride = _i8_operands(a, a8, a_scale, w8, w_scale)
     B = _requests(a, cu_seqlens)
     x_stride = 0 if x is None else a.rows("x", x, a.torch.bfloat16, (T, N))
@@ -666,8 +686,8 @@ def linear_i8_gated_residual(a8, a_scale, w8, w_scale, *, x=None, gate_res=None,
     out, out_stride = _rows_bf16(a, "out", out, (T, N))
     _check("pqk_linear_i8_gated_residual", lib().pqk_linear_i8_gated_residual(
         a8.data_ptr(), a_stride, a_scale.data_ptr(), w8.data_ptr(), w_stride, w_scale.data_ptr(), _ptr(x), x_stride,
-        _ptr(gate_res), _ptr(cu_seqlens), B, out.data_ptr(), out_stride, T, K, N, a.stream(stream)))
-    _used_on(a, stream, out)
+        _ptr(gate_res), _ptr(cu_seqlens), B, out.data_ptr(), out_stride, T, K, N, a.stream()))
+    a.used(out)
     return out
 
 
@@ -675,7 +695,7 @@ def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
     """act = silu(y[:, :F]) * y[:, F:] with y = a_scale * w_scale * (a8 @
     w8.T), the product in 8-bit integers. a8: int8 [T, K], w8: int8 [2F, K],
     a_scale fp32 [T], w_scale fp32 [2F]. Returns act bf16 [T, F]."""
-    a = _Args("linear_i8_swiglu")
+    a = _Args("linear_i8_swiglu", stream)
     T, K, rows, a_stride, w_stride = _i8_operands(a, a8, a_scale, w8, w_scale)
     F, odd = divmod(rows, 2)
     if odd:
@@ -683,8 +703,8 @@ def linear_i8_swiglu(a8, a_scale, w8, w_scale, *, act=None, stream=None):
     act, act_stride = _rows_bf16(a, "act", act, (T, F))
     _check("pqk_linear_i8_swiglu", lib().pqk_linear_i8_swiglu(
         a8.data_ptr(), a_stride, a_scale.data_ptr(), w8.data_ptr(), w_stride, w_scale.data_ptr(), act.data_ptr(),
-        act_stride, T, K, F, a.stream(stream)))
-    _used_on(a, stream, act)
+        act_stride, T, K, F, a.stream()))
+    a.used(act)
     return act
 
 
@@ -701,7 +721,7 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     0 to at most Tq and Tk (rows behind the last request are left as they
     are). A request without keys gives o = 0, lse = -inf. Returns (o, lse
     fp32 [H, Tq] or None)."""
-    a = _Args("varlen_cross_attn_fwd")
+    a = _Args("varlen_cross_attn_fwd", stream)
     torch, bf16 = a.torch, a.torch.bfloat16
     shape, q_stride = a.first("q", q, bf16, 3)
     Tq, H, D = shape
@@ -728,8 +748,8 @@ def varlen_cross_attn_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale:
     _check("pqk_varlen_cross_attn_fwd", lib().pqk_varlen_cross_attn_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), q_stride, k_stride, v_stride, o_stride,
         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq, Tk, H, Hkv, D, scale, workspace.data_ptr(),
-        workspace.nbytes, a.stream(stream)))
-    _used_on(a, stream, o, lse, workspace)
+        workspace.nbytes, a.stream()))
+    a.used(o, lse, workspace)
     return o, lse
 
 
