@@ -175,6 +175,18 @@ def _stream_object(stream):
     return cuda.ExternalStream(stream) if stream != 0 else cuda.default_stream()
 
 
+def _new(stream, shape, dtype, device):
+    """A new tensor for a call on `stream`, on that stream's account (see
+    _Args), and for the caller's current stream to read."""
+    torch = _torch or _load_torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_stream_object(stream)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 class _Args:
     """Checks of one call's tensors: type, shape, unit stride inside a row,
     and the current CUDA device (the library launches on it). What a call
@@ -352,11 +364,11 @@ def qk_norm_rope_e4m3(q, k, w_q, w_k, pos, *, eps: float = 1e-6, rope_base: floa
     import torch
     T, H, D = q.shape
     if q8 is None:
-        q8 = torch.empty((T, H, D), dtype=torch.uint8, device=q.device)
+        q8 = _new(stream, (T, H, D), torch.uint8, q.device)
     if k8 is None:
-        k8 = torch.empty((T, H, D), dtype=torch.uint8, device=q.device)
+        k8 = _new(stream, (T, H, D), torch.uint8, q.device)
     if deq is None:
-        deq = torch.empty(2 * H, dtype=torch.float32, device=q.device)
+        deq = _new(stream, 2 * H, torch.float32, q.device)
     assert q8.is_contiguous() and k8.is_contiguous() and deq.numel() >= 2 * H
     _check("pqk_qk_norm_rope_e4m3", lib().pqk_qk_norm_rope_e4m3(
         _ptr(q), _ptr(k), _ptr(q8), _ptr(k8), _token_stride(q, 3), _token_stride(k, 3), _ptr(w_q), _ptr(w_k),
@@ -408,12 +420,12 @@ def varlen_attn_fwd(q, k, v, cu_seqlens, *, softmax_scale: float | None = None, 
     B = cu_seqlens.shape[0] - 1
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
     if o is None:
-        o = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        o = _new(stream, (T, H, D), q.dtype, q.device)
     if lse is None and want_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, (H, T), torch.float32, q.device)
     ws_bytes = varlen_attn_workspace_size(B)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, ws_bytes, torch.uint8, q.device)
     _check("pqk_varlen_attn_fwd", lib().pqk_varlen_attn_fwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _token_stride(q, 3), _token_stride(k, 3),
         _token_stride(v, 3), _token_stride(o, 3), _ptr(cu_seqlens), B, T, H, D, scale, _ptr(workspace),
@@ -433,12 +445,12 @@ def varlen_attn_fwd_skip(q, k, v, cu_seqlens, skip_threshold_log2: float, *, sof
     B = cu_seqlens.shape[0] - 1
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
     if o is None:
-        o = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        o = _new(stream, (T, H, D), q.dtype, q.device)
     if lse is None and want_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, (H, T), torch.float32, q.device)
     ws_bytes = varlen_attn_workspace_size(B)
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, ws_bytes, torch.uint8, q.device)
     if skip_counts is not None:
         assert skip_counts.dtype == torch.int64 and skip_counts.numel() >= 2 and skip_counts.is_contiguous()
     _check("pqk_varlen_attn_fwd_skip", lib().pqk_varlen_attn_fwd_skip(
@@ -454,11 +466,11 @@ def quantize_qk_e4m3(q, k, *, q8=None, k8=None, scales=None, stream=None):
     import torch
     T, H, D = q.shape
     if q8 is None:
-        q8 = torch.empty((T, H, D), dtype=torch.uint8, device=q.device)
+        q8 = _new(stream, (T, H, D), torch.uint8, q.device)
     if k8 is None:
-        k8 = torch.empty((T, H, D), dtype=torch.uint8, device=q.device)
+        k8 = _new(stream, (T, H, D), torch.uint8, q.device)
     if scales is None:
-        scales = torch.empty(4 * H, dtype=torch.float32, device=q.device)
+        scales = _new(stream, 4 * H, torch.float32, q.device)
     assert q8.is_contiguous() and k8.is_contiguous() and scales.numel() >= 4 * H
     _check("pqk_quantize_qk_e4m3", lib().pqk_quantize_qk_e4m3(
         _ptr(q), _ptr(k), _token_stride(q, 3), _token_stride(k, 3), T, H, D, _ptr(q8), _ptr(k8), _ptr(scales),
@@ -478,11 +490,11 @@ def varlen_attn_fwd_fp8qk(q8, k8, v, deq, cu_seqlens, *, softmax_scale: float | 
     B = cu_seqlens.shape[0] - 1
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
     if o is None:
-        o = torch.empty((T, H, D), dtype=v.dtype, device=v.device)
+        o = _new(stream, (T, H, D), v.dtype, v.device)
     if lse is None and want_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=v.device)
+        lse = _new(stream, (H, T), torch.float32, v.device)
     if workspace is None:
-        workspace = torch.empty(varlen_attn_workspace_size(B), dtype=torch.uint8, device=v.device)
+        workspace = _new(stream, varlen_attn_workspace_size(B), torch.uint8, v.device)
     assert q8.is_contiguous() and k8.is_contiguous() and tuple(q8.shape) == (T, H, D) == tuple(k8.shape)
     _check("pqk_varlen_attn_fwd_fp8qk", lib().pqk_varlen_attn_fwd_fp8qk(
         _ptr(q8), _ptr(k8), _ptr(v), _ptr(deq), _ptr(o), _ptr(lse), _token_stride(v, 3), _token_stride(o, 3),
@@ -497,9 +509,9 @@ def quantize_e4m3(x, *, x8=None, scales=None, stream=None):
     import torch
     T, H, D = x.shape
     if x8 is None:
-        x8 = torch.empty((T, H, D), dtype=torch.uint8, device=x.device)
+        x8 = _new(stream, (T, H, D), torch.uint8, x.device)
     if scales is None:
-        scales = torch.empty(2 * H, dtype=torch.float32, device=x.device)
+        scales = _new(stream, 2 * H, torch.float32, x.device)
     assert x8.is_contiguous() and scales.numel() >= 2 * H
     _check("pqk_quantize_e4m3", lib().pqk_quantize_e4m3(_ptr(x), _token_stride(x, 3), T, H, D, _ptr(x8),
                                                          _ptr(scales), _stream(stream)))
@@ -518,11 +530,11 @@ def varlen_attn_fwd_fp8(q8, k8, v8, deq, cu_seqlens, *, softmax_scale: float | N
     B = cu_seqlens.shape[0] - 1
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
     if o is None:
-        o = torch.empty((T, H, D), dtype=torch.bfloat16, device=q8.device)
+        o = _new(stream, (T, H, D), torch.bfloat16, q8.device)
     if lse is None and want_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q8.device)
+        lse = _new(stream, (H, T), torch.float32, q8.device)
     if workspace is None:
-        workspace = torch.empty(varlen_attn_workspace_size(B), dtype=torch.uint8, device=q8.device)
+        workspace = _new(stream, varlen_attn_workspace_size(B), torch.uint8, q8.device)
     for t in (q8, k8, v8):
         assert t.is_contiguous() and tuple(t.shape) == (T, H, D)
     assert deq.is_contiguous() and deq.numel() >= 3 * H
@@ -546,9 +558,9 @@ def varlen_attn_fwd_noalloc(q, k, v, cu_seqlens, *, softmax_scale: float | None 
     B = cu_seqlens.shape[0] - 1
     scale = softmax_scale if softmax_scale is not None else D ** -0.5
     if o is None:
-        o = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        o = _new(stream, (T, H, D), q.dtype, q.device)
     if lse is None and want_lse:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        lse = _new(stream, (H, T), torch.float32, q.device)
     _check("pqk_varlen_attn_fwd_noalloc", lib().pqk_varlen_attn_fwd_noalloc(
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _token_stride(q, 3), _token_stride(k, 3),
         _token_stride(v, 3), _token_stride(o, 3), _ptr(cu_seqlens), B, T, H, D, scale, _stream(stream)))
@@ -559,18 +571,17 @@ def modulate_swiglu(x, shift, scale, cu_seqlens, *, gate_res=None, branch=None, 
                     norm_type: int = NORM_RMS, eps: float = 1e-6, x_out=None, h=None, act=None, stream=None):
     """Fused gated residual + norm + adaLN modulation, and SwiGLU.
     Returns (x_out or None, h, act or None)."""
-    import torch
     T, Cdim = x.shape
     B = cu_seqlens.shape[0] - 1
     if h is None:
-        h = torch.empty_like(x)
+        h = _new(stream, x.shape, x.dtype, x.device)
     F, gu_stride = 0, 0
     if gate is not None:
         F = gate.shape[1]
         gu_stride = _token_stride(gate, 2)
         assert _token_stride(up, 2) == gu_stride
         if act is None:
-            act = torch.empty((T, F), dtype=x.dtype, device=x.device)
+            act = _new(stream, (T, F), x.dtype, x.device)
     _check("pqk_modulate_swiglu", lib().pqk_modulate_swiglu(
         _ptr(x), _ptr(branch), _ptr(x_out), _ptr(h), _ptr(shift), _ptr(scale), _ptr(gate_res), _ptr(cu_seqlens),
         B, T, Cdim, norm_type, eps, _ptr(gate), _ptr(up), gu_stride, _ptr(act), F, _stream(stream)))
@@ -582,12 +593,11 @@ def linear_gated_residual(a, w, *, x=None, gate_res=None, cu_seqlens=None, out=N
     residual add in the GEMM's epilogue); with x None the product alone.
     a: [T, K] bf16 (rows may be strided), w: [N, K] bf16, x: [T, N] bf16,
     gate_res: [B, N] fp32. out may be x (in place)."""
-    import torch
     T, K = a.shape
     N = w.shape[0]
     assert w.shape == (N, K) and w.is_contiguous()
     if out is None:
-        out = torch.empty((T, N), dtype=a.dtype, device=a.device)
+        out = _new(stream, (T, N), a.dtype, a.device)
     B = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
     x_stride = 0 if x is None else _token_stride(x, 2)
     _check("pqk_linear_gated_residual", lib().pqk_linear_gated_residual(
@@ -599,12 +609,11 @@ def linear_gated_residual(a, w, *, x=None, gate_res=None, cu_seqlens=None, out=N
 def linear_swiglu(a, w1, *, act=None, stream=None):
     """act = silu(a @ w1[:F].T) * (a @ w1[F:].T) on the tensor cores (SwiGLU
     in the GEMM's epilogue). a: [T, K] bf16, w1: [2F, K] bf16."""
-    import torch
     T, K = a.shape
     F = w1.shape[0] // 2
     assert w1.shape == (2 * F, K) and w1.is_contiguous()
     if act is None:
-        act = torch.empty((T, F), dtype=a.dtype, device=a.device)
+        act = _new(stream, (T, F), a.dtype, a.device)
     _check("pqk_linear_swiglu", lib().pqk_linear_swiglu(
         _ptr(a), _token_stride(a, 2), _ptr(w1), _ptr(act), _token_stride(act, 2), T, K, F, _stream(stream)))
     return act

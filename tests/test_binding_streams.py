@@ -75,7 +75,12 @@ class Tensor:
         self.readers.append(s)
 
     def __getitem__(self, index):
-        t = Tensor(self.dtype, (self.shape[0], index[1].stop), self._strides, self.owner)
+        """A range of a vector, or the first columns of a matrix's rows."""
+        if isinstance(index, slice):
+            shape = (len(range(*index.indices(self.shape[0]))),)
+        else:
+            shape = (self.shape[0], index[1].stop)
+        t = Tensor(self.dtype, shape, self._strides, self.owner)
         t.ptr, t.readers = self.ptr, self.readers
         return t
 
@@ -196,3 +201,40 @@ def test_the_callers_tensors_are_recorded_on_the_calls_stream(fake):
     x8, scales = Tensor("int8", (4, 64)), Tensor("float32", (4,))
     pqk.quantize_i8(_bf(4, 64), x8=x8, scales=scales, stream=Stream(7))
     assert not fake[0].made and Stream(7) in x8.readers and Stream(7) in scales.readers
+
+
+def _f32(*shape):
+    return Tensor("float32", shape)
+
+
+def _u8(*shape):
+    return Tensor("uint8", shape)
+
+
+CALLS = {
+    "qk_norm_rope_e4m3": lambda s: pqk.qk_norm_rope_e4m3(_bf(4, 2, 128), _bf(4, 2, 128), _bf(128), _bf(128), _cu(4),
+                                                         stream=s),
+    "varlen_attn_fwd": lambda s: pqk.varlen_attn_fwd(_bf(4, 2, 64), _bf(4, 2, 64), _bf(4, 2, 64), _cu(3),
+                                                     want_lse=True, stream=s),
+    "varlen_attn_fwd_skip": lambda s: pqk.varlen_attn_fwd_skip(_bf(4, 2, 64), _bf(4, 2, 64), _bf(4, 2, 64), _cu(3),
+                                                               8.0, want_lse=True, stream=s),
+    "quantize_qk_e4m3": lambda s: pqk.quantize_qk_e4m3(_bf(4, 2, 128), _bf(4, 2, 128), stream=s),
+    "varlen_attn_fwd_fp8qk": lambda s: pqk.varlen_attn_fwd_fp8qk(
+        _u8(4, 2, 128), _u8(4, 2, 128), _bf(4, 2, 128), _f32(4), _cu(3), want_lse=True, stream=s),
+    "quantize_e4m3": lambda s: pqk.quantize_e4m3(_bf(4, 2, 128), stream=s),
+    "varlen_attn_fwd_fp8": lambda s: pqk.varlen_attn_fwd_fp8(
+        _u8(4, 2, 128), _u8(4, 2, 128), _u8(4, 2, 128), _f32(6), _cu(3), want_lse=True, stream=s),
+    "varlen_attn_fwd_noalloc": lambda s: pqk.varlen_attn_fwd_noalloc(
+        _bf(4, 2, 64), _bf(4, 2, 64), _bf(4, 2, 64), _cu(3), want_lse=True, stream=s),
+    "modulate_swiglu": lambda s: pqk.modulate_swiglu(_bf(4, 64), _f32(2, 64), _f32(2, 64), _cu(3), gate=_bf(4, 64),
+                                                     up=_bf(4, 64), stream=s),
+    "linear_gated_residual": lambda s: pqk.linear_gated_residual(_bf(4, 64), _bf(32, 64), stream=s),
+    "linear_swiglu": lambda s: pqk.linear_swiglu(_bf(4, 64), _bf(32, 64), stream=s),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_new_tensors_of_the_bf16_and_fp8_calls(fake, name):
+    for stream, handle in ((Stream(7), 7), (9, 9), (0, 0), (None, 0)):
+        fake[0].made.clear()
+        _check(fake, CALLS[name], stream, handle)
