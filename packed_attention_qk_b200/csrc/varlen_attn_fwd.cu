@@ -1405,6 +1405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           v_idx = next_v;
           nk_idx = next_nk;
         }
+        if (!ok) break;  // no product of another unit after a wait that ran out
       }
       if (kSkip && p.skip_counts != nullptr && pv_skips != 0) atomicAdd(&p.skip_counts[1], pv_skips);
       if (!ok) abort_all();
