@@ -555,7 +555,9 @@ PQK_API int pqk_linear_i8_swiglu(const void* a8, int64_t a8_stride_t, const floa
  * enters by cross-attention is a reading.
  *   O = softmax(softmax_scale * Q K^T) V over the request's keys, bf16
  *   operands, fp32 accumulation, probabilities rounded to bf16 for P V.
- * A request without keys gives O = 0 and lse = -inf for its queries.
+ * A request without keys gives O = 0 and lse = -inf for its queries. Keys whose
+ * score is -inf (keys with infinities) weigh nothing; a query whose scores are
+ * all -inf has O = NaN (0 / 0) and lse = -inf.
  *
  * q, o          device bf16 [Tq, H, D]; k, v device bf16 [Tk, Hkv, D], Hkv a
  *               divisor of H (query head h reads key head h / (H / Hkv)), rows

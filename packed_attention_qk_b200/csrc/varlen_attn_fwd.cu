@@ -647,6 +647,11 @@ __global__ void __launch_bounds__(32)
 // O = sum_i 2^(u_i - u) o_i / sum_i 2^(u_i - u) with u the largest u_i, and
 // lse = (u + log2 of that sum) ln 2. Block (x, y) takes tile x's rows from 8 y
 // on, a warp a row, the parts in order.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 constexpr int kCombineThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
@@ -678,9 +683,9 @@ __global__ void __launch_bounds__(kCombineThreads)
     const float* u = part_lse + row0;
     const float* src = part_o + row0 * D + lane * (D / 32);
     float top = -INFINITY;
-    for (int k = lane; k < n; k += 32) top = fmaxf(top, u[k * step]);
+    for (int k = lane; k < n; k += 32) top = max_or_nan(top, u[k * step]);
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    for (int off = 16; off >= 1; off >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
     float sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
@@ -708,7 +713,8 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     if (lse != nullptr && lane == 0)
-      lse[static_cast<int64_t>(head) * Tq + t] = (top + __log2f(sum)) * 0.69314718055994530942f;
+      lse[static_cast<int64_t>(head) * Tq + t] =
+          top == -INFINITY ? top : (top + __log2f(sum)) * 0.69314718055994530942f;  // no part has a finite score
   }
 }
 
@@ -1489,7 +1495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool need_rescale = j >= step_j && mx > m + kRescaleThreshold;
         float alpha = 1.0f;
         if (j < step_j) {
-          m = mx;
+          // kCross: a first key tile of scores -inf alone (keys with infinities)
+          // leaves P = 0 and l = 0 behind, not exp(-inf + inf)
+          m = kCross ? fmaxf(mx, -3.402823466e38f) : mx;
         } else if (need_rescale) {
           alpha = ex2_approx(m - mx);
           l *= alpha;
@@ -1567,6 +1575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (un.slot >= 0) {
           const int64_t prow = static_cast<int64_t>(un.slot) * kRowsPerWork + grp * kBM + r;
           float4* part = reinterpret_cast<float4*>(p.part_o + prow * D);
+          // a part whose scores are all -inf: rows of 0, to be joined with weight 0
+          const float part_inv_l = l == 0.f ? 0.f : inv_l;
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t ov[32];
@@ -1575,8 +1585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 32; c += 4)
                 part[(c0 + c) / 4] =
-                    make_float4(__uint_as_float(ov[c]) * inv_l, __uint_as_float(ov[c + 1]) * inv_l,
-                                __uint_as_float(ov[c + 2]) * inv_l, __uint_as_float(ov[c + 3]) * inv_l);
+                    make_float4(__uint_as_float(ov[c]) * part_inv_l, __uint_as_float(ov[c + 1]) * part_inv_l,
+                                __uint_as_float(ov[c + 2]) * part_inv_l, __uint_as_float(ov[c + 3]) * part_inv_l);
             }
           }
           if (valid_row) p.part_lse[prow] = m + __log2f(l);
