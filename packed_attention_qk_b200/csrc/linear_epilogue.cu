@@ -66,6 +66,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "packed_rows.cuh"
 #include "pqk_internal.h"
 
 namespace pqk {
@@ -141,29 +142,10 @@ __device__ __forceinline__ TileCoord tile_coord(int i, int m_tiles, int n_tiles)
   return c;
 }
 
-__device__ __forceinline__ int request_of(const int32_t* cu, int B, int64_t t) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(__ldg(cu + mid)) <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
 __device__ __forceinline__ uint4 ld_nc16(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
-}
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
-// Four neighbouring int32 sums of a token times its scale and theirs.
-__device__ __forceinline__ void scaled4(int4 sum, float row_scale, float4 w, float (&y)[4]) {
-  y[0] = __int2float_rn(sum.x) * row_scale * w.x;
-  y[1] = __int2float_rn(sum.y) * row_scale * w.y;
-  y[2] = __int2float_rn(sum.z) * row_scale * w.z;
-  y[3] = __int2float_rn(sum.w) * row_scale * w.w;
 }
 
 // The kI8 epilogue of one warp: 32 rows from row0 on, its half of the tile's
@@ -267,10 +249,7 @@ __device__ __forceinline__ bool store_rows_i8(const Params& p, uint32_t t_acc, u
         if (!one_request)
           g = __ldg(reinterpret_cast<const float4*>(
               p.gate_res + static_cast<int64_t>(request_of(p.cu, p.B, row)) * p.N + col));
-        y[0] = fmaf(g.x, y[0], bf16_lo(x[c][i].x));
-        y[1] = fmaf(g.y, y[1], bf16_hi(x[c][i].x));
-        y[2] = fmaf(g.z, y[2], bf16_lo(x[c][i].y));
-        y[3] = fmaf(g.w, y[3], bf16_hi(x[c][i].y));
+        gated4(x[c][i], g, y);
       }
       *reinterpret_cast<uint2*>(p.out + row * p.out_stride + col) =
           make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));

@@ -30,6 +30,7 @@
 
 #include <cstdint>
 
+#include "packed_rows.cuh"
 #include "pqk_internal.h"
 
 namespace pqk {
@@ -75,25 +76,6 @@ struct Params {
   int* status;
   long long timeout_ns;
 };
-
-__device__ __forceinline__ int request_of(const int32_t* cu, int B, int64_t t) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(__ldg(cu + mid)) <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
-// Four neighbouring sums times the token's and the rows' scales.
-__device__ __forceinline__ void scaled4(int4 s, float row_scale, const float* ws, float (&y)[4]) {
-  const float4 w = __ldg(reinterpret_cast<const float4*>(ws));
-  y[0] = __int2float_rn(s.x) * row_scale * w.x;
-  y[1] = __int2float_rn(s.y) * row_scale * w.y;
-  y[2] = __int2float_rn(s.z) * row_scale * w.z;
-  y[3] = __int2float_rn(s.w) * row_scale * w.w;
-}
 
 template <int kNT, int kEpi>
 __global__ void __launch_bounds__(kThreads)
@@ -256,20 +238,16 @@ __global__ void __launch_bounds__(kThreads)
         }
         const float row_scale = __ldg(p.a_scale + t);
         float y[4];
-        scaled4(sum, row_scale, p.w_scale + col, y);
+        scaled4(sum, row_scale, __ldg(reinterpret_cast<const float4*>(p.w_scale + col)), y);
         if constexpr (kEpi == kEpiSwiglu) {
           float u[4];
-          scaled4(up, row_scale, p.w_scale + p.N + col, u);
+          scaled4(up, row_scale, __ldg(reinterpret_cast<const float4*>(p.w_scale + p.N + col)), u);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = silu_mul(y[e], u[e]);
         } else if constexpr (kEpi == kEpiGatedResidual) {
           const int64_t g0 = static_cast<int64_t>(request_of(p.cu, p.B, t)) * p.N + col;
           const float4 g = __ldg(reinterpret_cast<const float4*>(p.gate_res + g0));
-          const uint2 xv = *reinterpret_cast<const uint2*>(p.x + t * p.x_stride + col);
-          y[0] = fmaf(g.x, y[0], __uint_as_float(xv.x << 16));
-          y[1] = fmaf(g.y, y[1], __uint_as_float(xv.x & 0xFFFF0000u));
-          y[2] = fmaf(g.z, y[2], __uint_as_float(xv.y << 16));
-          y[3] = fmaf(g.w, y[3], __uint_as_float(xv.y & 0xFFFF0000u));
+          gated4(*reinterpret_cast<const uint2*>(p.x + t * p.x_stride + col), g, y);
         }
         *reinterpret_cast<uint2*>(p.out + t * p.out_stride + col) =
             make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));

@@ -29,6 +29,7 @@
 #include <climits>
 #include <cstdint>
 
+#include "packed_rows.cuh"
 #include "pqk_internal.h"
 
 namespace pqk {
@@ -96,17 +97,6 @@ __device__ __forceinline__ void load8f(const float* p, bool wide, float (&f)[8])
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// Request s with cu[s] <= t < cu[s+1] (the last such s when requests are
-// empty); always in 0..B-1, whatever cu holds.
-__device__ __forceinline__ int find_segment(const int32_t* cu, int B, int64_t t) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(__ldg(cu + mid)) <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 // The kTpr threads of a row: combine one value of each and give every thread
 // the result. `slot`: kTpr / 32 words of shared memory used by this row only,
 // and by this exchange only until the row's next barrier.
@@ -159,7 +149,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
   if (t >= p.T) return;  // a whole row's threads leave together: barriers count one row's threads
   const int nchunks = p.C >> 3;
   const int64_t mod_row =
-      !kPlain && p.cu != nullptr ? static_cast<int64_t>(find_segment(p.cu, p.B, t)) * p.C : 0;
+      !kPlain && p.cu != nullptr ? static_cast<int64_t>(request_of(p.cu, p.B, t)) * p.C : 0;
 
   uint4 xr[kCpt];
 #pragma unroll

@@ -313,8 +313,6 @@ __device__ __forceinline__ CrossWork decode_cross(const int32_t* sched, int pack
 }
 
 // What the pipeline's roles ask of a unit of either kind.
-__device__ __forceinline__ int first_key(const Work& wk) { return wk.seg_start; }
-__device__ __forceinline__ int first_key(const CrossWork& wk) { return wk.k_start; }
 __device__ __forceinline__ int key_count(const Work& wk) { return wk.seg_len; }
 __device__ __forceinline__ int key_count(const CrossWork& wk) { return wk.k_len; }
 __device__ __forceinline__ int end_of_queries(const Work& wk) { return wk.seg_start + wk.seg_len; }
@@ -1977,7 +1975,6 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
                              float softmax_scale, void* workspace, int* status, long long timeout_ns,
                              cudaStream_t stream, int num_sms) {
   CUtensorMap tq, tk, tv;
-  // without any key there is nothing to map: the maps are never read then
   // all settings on the first call on a device: a later one, of other sizes, may be under capture
   if (!set_smem_attr<64, false, false, false, true>() || !set_smem_attr<128, false, false, false, true>() ||
       !set_schedule_smem_attr<true>())
@@ -1991,7 +1988,7 @@ int launch_varlen_cross_attn(const void* q, const void* k, const void* v, void* 
   if (!make_qkv_map(&tq, q, Tq, H, D, q_stride, tile_q, pack)) return -2;
   if (Tk > 0 ? !make_qkv_map(&tk, k, Tk, Hkv, D, k_stride) || !make_qkv_map(&tv, v, Tk, Hkv, D, v_stride) : false)
     return -2;
-  if (Tk == 0) tk = tv = tq;
+  if (Tk == 0) tk = tv = tq;  // without any key there is nothing to map, and these are not read
   int32_t* sched = static_cast<int32_t*>(workspace);
   int sort_n = 1;
   while (sort_n < B) sort_n <<= 1;
