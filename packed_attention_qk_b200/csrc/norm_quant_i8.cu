@@ -124,15 +124,30 @@ struct MaxOp {
 
 // Threads per block: one row, or four of a warp each (blocks of two or four
 // rows of 128 threads leave more of an SM idle between rows: 364 and 491 us
-// where these take 348 for [58,048, 5,120]). And the blocks per SM that the
-// registers have to allow where the compiler would use more: 40 registers for
-// 512 threads on x alone (12,345 rows of 16,384: 118 -> 105 us, of 14,344: 113 ->
-// 98), 72 with 5 chunks of everything (58,048 rows of 5,120: 357 -> 348 us,
-// without the branch 250 -> 233).
+// where these take 348 for [58,048, 5,120]).
 template <int kTpr>
 constexpr int kBlock = kTpr < 128 ? 128 : kTpr;
+
+// Blocks per SM that a layout's registers have to allow, where the compiler by
+// itself takes a few more registers than fit one more block of rows in flight
+// (four or more chunks a thread): at most 64 to 80 of them. Without and with the
+// bound, us, everything on / without the branch / LayerNorm without vectors:
+//   128 x 4  20,000 x 4,096   112 / 75 / 104   111 / 72 / 100
+//   128 x 5  58,048 x 5,120   389 / 259 / 363  377 / 245 / 353
+//   128 x 6  20,000 x 6,144   173 / 117 / 158  165 / 105 / 147
+//   128 x 7  20,000 x 7,168   222 / 130 / 188  222 / 125 / 175
+//   256 x 5  20,000 x 10,240  307 / 189 / 258  302 / 176 / 247
+//   256 x 6  12,345 x 12,288  274 / 173 / 217  257 / 137 / 189
+//   256 x 7  12,345 x 14,336  334 / 194 / 259  315 / 166 / 230 (32 bytes spilled)
+//   512 x 4  12,345 x 16,384  441 / 305 / 368  332 / 195 / 272
+// and for codes of x alone 512 x 4, 12,345 x 16,384 118 -> 105, x 14,344 113 -> 98.
 template <int kTpr, int kCpt, bool kPlain>
-constexpr int kBlocksPerSm = kPlain && kTpr == 512 ? 3 : (!kPlain && kTpr == 128 && kCpt == 5 ? 7 : 1);
+constexpr int kBlocksPerSm = kPlain      ? (kTpr == 512 ? 3 : 1)
+                             : kCpt < 4  ? 1
+                             : kTpr == 128 ? (kCpt == 4 ? 8 : kCpt == 7 ? 6 : 7)
+                             : kTpr == 256 ? (kCpt < 6 ? 4 : 3)
+                             : kTpr == 512 ? 2
+                                           : 1;
 
 // kPlain: codes of x alone (no branch, norm or vectors), in fewer registers.
 template <int kTpr, int kCpt, bool kPlain>
