@@ -97,6 +97,14 @@ __device__ __forceinline__ void load8f(const float* p, bool wide, float (&f)[8])
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+// The larger of a and |b|; NaN where one of them is. One instruction, where the
+// maximum of the bits takes two.
+__device__ __forceinline__ float max_abs_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
 // The kTpr threads of a row: combine one value of each and give every thread
 // the result. `slot`: kTpr / 32 words of shared memory used by this row only,
 // and by this exchange only until the row's next barrier.
@@ -131,7 +139,8 @@ constexpr int kBlock = kTpr < 128 ? 128 : kTpr;
 // Blocks per SM that a layout's registers have to allow, where the compiler by
 // itself takes a few more registers than fit one more block of rows in flight
 // (four or more chunks a thread): at most 64 to 80 of them. Without and with the
-// bound, us, everything on / without the branch / LayerNorm without vectors:
+// bound, us at one stage of the kernel, everything on / without the branch /
+// LayerNorm without vectors:
 //   128 x 4  20,000 x 4,096   112 / 75 / 104   111 / 72 / 100
 //   128 x 5  58,048 x 5,120   389 / 259 / 363  377 / 245 / 353
 //   128 x 6  20,000 x 6,144   173 / 117 / 158  165 / 105 / 147
@@ -271,6 +280,7 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
     }
   }
   uint32_t top = 0;  // bits of the largest |h|
+  float top_f = 0.f;
 #pragma unroll
   for (int i = 0; i < kCpt; ++i) {
     const int c = lane + i * kTpr;
@@ -292,10 +302,11 @@ __global__ void __launch_bounds__(kBlock<kTpr>, kBlocksPerSm<kTpr, kCpt, kPlain>
           for (int e = 0; e < 8; ++e) v[i][e] = fmaf(v[i][e], 1.0f + sc[e], sh[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7fffffffu);
+        for (int e = 0; e < 8; ++e) top_f = max_abs_or_nan(top_f, v[i][e]);
       }
     }
   }
+  if constexpr (!kPlain) top = __float_as_uint(top_f);
   top = row_reduce<kTpr>(top, s_max[group], MaxOp());
 
   const bool finite = top < 0x7f800000u;
