@@ -711,8 +711,10 @@ int launch_linear_i8(int epi, const void* a8, int64_t a_stride, const float* a_s
                      long long timeout_ns, cudaStream_t stream, int num_sms) {
   if (!prepare_i8(stream)) return -1;
   // Which kernel. Few tokens are W's bytes: the kernel with W on the M side is
-  // ahead whatever N is (T = 32, K = 5,120 -> SwiGLU 13,824: 27.7 against 35.7
-  // us). More tokens are not, but leave most SMs without a tile of 256 x 256:
+  // ahead whatever N is (us, small tiles / pairs: 32 tokens, 5,120 -> SwiGLU
+  // 13,824 27.9 / 36.7; 64 tokens, the same 30.2 / 37.4, 13,824 -> 5,120 20.1 /
+  // 40.6, 2,048 -> 13,824 11.0 / 11.7, 1,024 -> 27,648 11.0 / 13.5; 65 tokens, a
+  // tile more, 1,024 -> 27,648 14.0 / 13.5). More tokens are not, but leave most SMs without a tile of 256 x 256:
   // up to a tile for every third pair of SMs the smaller tiles with K split
   // over a cluster win (256 x 5,120 x 5,120, 20 tiles: 15.9 against 18.4 us;
   // 512 x 2,048 x 2,048, 16 tiles: 9.2 / 11.4; 1,024 x 2,048 x 2,048, 32
