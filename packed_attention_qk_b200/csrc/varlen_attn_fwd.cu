@@ -467,9 +467,10 @@ __global__ void __launch_bounds__(kSchedThreads) build_schedule_kernel(const int
 }
 
 // Tiles are cut along their keys when there are fewer of them than this (one
-// B200's SMs): into parts of at most as many key tiles as make the units no
-// more than the SMs, but kMinPartTiles at least (a part costs its rows' way
-// through the workspace).
+// B200's SMs; a constant, since the workspace's size is given by B and D alone
+// and holds a slot for each part): into parts of at most as many key tiles as
+// make the units no more than that, but kMinPartTiles at least (a part costs its
+// rows' way through the workspace).
 constexpr int kCutUnits = 148;
 constexpr int kMinPartTiles = 4;
 
@@ -780,7 +781,12 @@ __device__ __forceinline__ void exp4(const float (&s)[128], int c, float scale_l
 // and written over the first 64 columns of S at `t_p` (tensor memory), or,
 // with kE4m3P, rounded to e4m3 (four per column) over the first 32; returns
 // their unrounded fp32 sum. Waits for its tensor-memory stores before
-// returning.
+// returning. bf16 is V's type, and kind::f16 takes both operands of P V in one
+// type; tf32 would keep more of P at half the MMA rate and twice P's columns.
+// A probability is off by at most half a step, 2^-8 of itself, so O moves by at
+// most that share of sum p |v|; measured on cross-attention, the output's
+// relative distance from the 64-bit definition is 0.0020-0.0023 instead of the
+// 0.0017 of rounding O alone.
 template <bool kE4m3P>
 __device__ __forceinline__ float exp_tile_store(const float (&s)[128], float scale_log2, float neg_m, uint32_t t_p) {
   float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
