@@ -124,3 +124,27 @@ def test_halves_of_the_maximum_after_a_norm(T, C):
         torch.cuda.synchronize()
         c = c.cpu().numpy()
         assert (c[:, 3] == 127).all() and (c[:, 8::11] == 64).all() and (c[:, 9::11] == -64).all()
+
+
+@pytest.mark.parametrize("T", [7, 900])
+@pytest.mark.parametrize("C", [256, 5120, 16384])
+@pytest.mark.parametrize("exponent", [-120, -112, 87, 110])
+def test_sums_near_the_ends_of_the_range(T, C, exponent):
+    """The same whole numbers times a power of two: maxima on both sides of 2^-100 and 2^100, in one call. Their scale
+    is the maximum over 127, rounded once."""
+    torch = torch_cuda()
+    g = np.random.default_rng([T, C, exponent + 200])
+    a, b = g.integers(-128, 129, (T, C)).astype(np.float64), 128.0 * g.integers(-20, 21, (T, C))
+    a[:, 0], b[:, 0] = np.where(np.arange(T) % 3 == 0, 97.0, g.integers(0, 129, T)), 128.0 * 30
+    a[::3, 1::5], b[::3, 1::5] = 31.0 * g.integers(0, 4, a[::3, 1::5].shape), 0.0
+    unit = 2.0 ** (exponent + np.arange(T) % 5)[:, None]
+    a, b = a * unit, b * unit
+    h = a + b
+    x, br = _bits(a), _bits(b)
+    assert np.array_equal(wl.bf16_bits_to_f64(x) + wl.bf16_bits_to_f64(br), h)
+    xo = torch.empty(T, C, dtype=torch.bfloat16, device="cuda")
+    _, c, s = pqk.norm_modulate_i8(to_dev_bf16(x), branch=to_dev_bf16(br), x_out=xo, norm_type=pqk.NORM_NONE)
+    torch.cuda.synchronize()
+    assert np.array_equal(c.cpu().numpy(), exact_codes(h))
+    assert np.array_equal(s.cpu().numpy(), np.abs(h).max(axis=1).astype(np.float32) / np.float32(127))
+    assert np.array_equal(bf16_to_f64(xo), wl.bf16_bits_to_f64(_bits(h)))

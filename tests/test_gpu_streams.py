@@ -42,3 +42,22 @@ def test_outputs_are_not_memory_that_the_current_stream_still_writes(raw):
     pqk.quantize_i8(torch.zeros_like(x), stream=side)
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+def test_the_default_streams_handle():
+    """Handle 0 is the default stream, also while another stream is the current one."""
+    torch = torch_cuda()
+    x = torch.randn(300, 264, device="cuda").to(torch.bfloat16)
+    want = pqk.quantize_i8(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        got = pqk.quantize_i8(x, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    q = torch.randn(70, 2, 64, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, 20, 70], dtype=torch.int32, device="cuda")
+    o, _ = pqk.varlen_cross_attn_fwd(q, q, q, cu, cu)
+    o0, _ = pqk.varlen_cross_attn_fwd(q, q, q, cu, cu, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o0) and pqk.get_device_status() == 0
