@@ -624,7 +624,8 @@ def norm_modulate_i8(x, *, branch=None, gate_res=None, weight=None, shift=None, 
     """Gated residual + norm + adaLN modulation with an int8 output and one
     scale per token: x' = x + gate_res[request] * branch (without gate_res:
     x + branch), h = norm(x') * weight * (1 + scale[request]) +
-    shift[request], h8 = round(h / h_scale), h_scale = max |h| / 127.
+    shift[request], h8 = round(127 h / max |h|), ties to even, h_scale =
+    max |h| / 127.
     x, branch, x_out: bf16 [T, C] (rows may be strided; x_out may be x);
     weight bf16 [C]; gate_res, shift, scale fp32 [B, C]; cu_seqlens int32
     [B+1]. Returns (x_out or None, h8 int8 [T, C], h_scale fp32 [T])."""
